@@ -1,4 +1,4 @@
-// K3 fast path: decode / dequantise for widths that are multiples of 256
+// K3 fast path: decode / dequantise for widths up to 14,336, multiples of 256
 // ("E8-QAT", abstract: the core encoding and the sparse extension keep the
 // selected lattice points exactly).
 //

@@ -424,11 +424,11 @@ e8q_status e8q_decode(const e8q_encoded* m, int32_t basis, void* out_bf16, e8q_s
     p.cols = static_cast<int32_t>(m->cols);
     p.logb = logb;
     p.basis = basis;
-    // fast path (original basis through the register Hadamard, B >= 256); its
-    // staging warp copies indices in 16-byte words and overflow group ids in
-    // 4-byte words
+    // fast path (original basis through the register Hadamard, B >= 256) for
+    // rows that fit its tile; its staging warp copies indices in 16-byte words
+    // and overflow group ids in 4-byte words
     const bool orig = basis == E8Q_DEQUANT_ORIGINAL;
-    if (p.cols % 256 == 0 && (!orig || logb >= 8) && (reinterpret_cast<uintptr_t>(p.idx) & 15) == 0 &&
+    if (p.cols % 256 == 0 && p.cols <= kDfTileElems && (!orig || logb >= 8) && (reinterpret_cast<uintptr_t>(p.idx) & 15) == 0 &&
         (reinterpret_cast<uintptr_t>(p.ovf) & 3) == 0) {
         p.rpt = decode_fast_rows_per_tile(p.cols);
         p.n_tiles = (p.rows + p.rpt - 1) / p.rpt;
