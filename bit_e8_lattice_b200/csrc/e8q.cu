@@ -2,6 +2,7 @@
 // Argument checks, per-device constant tables, workspace sizing, launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -11,10 +12,12 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "decode_fast.cuh"
+#include "decode_rows.cuh"
 #include "encode.cuh"
 #include "encode_fast.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
+#include "rows_backward.cuh"
 #include "ste.cuh"
 #include "tables.h"
 
@@ -86,6 +89,16 @@ e8q_status ensure_device(int* dev_out) {
             }
             st = cuda_ok(cudaMemcpyToSymbol(g_gv_tab, words.data(), words.size() * sizeof(uint32_t)));
         }
+        // the row lookup of the widest rows holds more than the default 48 KB with its signs
+        const int dr_smem = static_cast<int>(dr_smem_bytes(true, kMaxCols));
+        if (st == E8Q_OK)
+            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
+        if (st == E8Q_OK)
+            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
+        if (st == E8Q_OK)
+            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
+        if (st == E8Q_OK)
+            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
         if (st == E8Q_OK)
             st = cuda_ok(cudaFuncSetAttribute(k_gv_main<1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmemBytes));
         if (st == E8Q_OK)
@@ -219,6 +232,63 @@ bool gemm_plan(const e8q_encoded* m, int32_t batch, int logb, GmGeom* g) {
     *g = gm_geometry(m->rows, m->cols, batch, logb);
     return g->nunits >= 0;
 }
+
+// Row-gradient plan: what depends on the shapes only.
+struct RbPlan {
+    int64_t slices;      // of kRbSliceCols columns
+    int64_t chunk;       // sorted tokens a summing CTA
+    int64_t chunks;
+    int64_t radix_ctas;  // 0: no radix sort
+    size_t keys[2], order[2], hist, part;
+    size_t total;  // workspace; enough for fewer ids too
+};
+
+RbPlan rb_plan(int64_t n, int64_t cols) {
+    RbPlan r = {};
+    r.slices = (cols + kRbSliceCols - 1) / kRbSliceCols;
+    r.chunk = kRbMaxChunk;
+    // at least four summing CTAs for each of 148 SMs where the batch allows it;
+    // a constant, so that the order of the sums is the same on any device
+    constexpr int64_t kWant = 4 * 148;
+    while (r.chunk > 8 && (n + r.chunk - 1) / r.chunk * r.slices < kWant) r.chunk /= 2;
+    r.chunks = (n + r.chunk - 1) / r.chunk;
+    // chunks of any n' <= n: a chunk below the longest was halved from one that gave fewer than kWant / slices
+    int64_t most = 2 * (kWant / r.slices + 1);
+    if (most > (n + 7) / 8) most = (n + 7) / 8;
+    if (most < (n + kRbMaxChunk - 1) / kRbMaxChunk) most = (n + kRbMaxChunk - 1) / kRbMaxChunk;
+    if (n <= kRbDirectMax) {
+        r.total = 256;
+        return r;
+    }
+    size_t at = 0;
+    auto take = [&at](size_t bytes) {
+        const size_t o = at;
+        at += align256(bytes);
+        return o;
+    };
+    const bool radix = n > kRbRankMax;
+    r.radix_ctas = radix ? (n + kRbTile - 1) / kRbTile : 0;
+    for (int i = 0; i < (radix ? 2 : 1); ++i) {
+        r.keys[i] = take(static_cast<size_t>(n) * 4);
+        r.order[i] = take(static_cast<size_t>(n) * 4);
+    }
+    r.hist = take(static_cast<size_t>(r.radix_ctas) * kRbBins * 4);
+    r.part = take(static_cast<size_t>(most) * 2 * cols * 4);
+    r.total = at;
+    return r;
+}
+
+bool valid_dtype(int32_t t) { return t == E8Q_F32 || t == E8Q_BF16; }
+bool valid_id_type(int32_t t) { return t == E8Q_I32 || t == E8Q_I64; }
+size_t dtype_bytes(int32_t t) { return t == E8Q_F32 ? 4 : 2; }
+size_t id_bytes(int32_t t) { return t == E8Q_I32 ? 4 : 8; }
+
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bn && y < x + an;
+}
+
+constexpr int64_t kMaxIds = int64_t{1} << 30;
 
 }  // namespace
 }  // namespace e8q
@@ -647,6 +717,173 @@ e8q_status e8q_ste_backward(const void* grad_dequant, void* grad_latent, int64_t
                                                  static_cast<uint16_t*>(grad_latent), n);
     }
     return cuda_ok(cudaGetLastError());
+}
+
+e8q_status e8q_decode_rows(const e8q_encoded* m, int32_t basis, const void* ids, int32_t id_type, int64_t n,
+                           int64_t first_row, float alpha, void* out, int32_t out_dtype, e8q_stream stream) {
+    int logb;
+    e8q_status st = check_encoded(m, &logb);
+    if (st != E8Q_OK) return st;
+    if (basis != E8Q_DEQUANT_ROTATED && basis != E8Q_DEQUANT_ORIGINAL) return E8Q_ERR_INVALID_ARG;
+    if (n < 0 || !valid_id_type(id_type) || !valid_dtype(out_dtype) || !std::isfinite(alpha)) return E8Q_ERR_INVALID_ARG;
+    if (n > kMaxIds || m->group_base + m->rows * (m->cols / 8) > (int64_t{1} << 32)) return E8Q_ERR_UNSUPPORTED;
+    if (n == 0) return E8Q_OK;
+    if (!ids || !out || !aligned(ids, id_bytes(id_type)) || !aligned(out, 16)) return E8Q_ERR_INVALID_ARG;
+    if (m->rows > 0) {
+        if (!aligned(m->idx, 2) || !aligned(m->scale, 4)) return E8Q_ERR_INVALID_ARG;
+        if (basis == E8Q_DEQUANT_ORIGINAL && (!m->signs || !aligned(m->signs, 8))) return E8Q_ERR_INVALID_ARG;
+        if (m->esc_row_ptr && !aligned(m->esc, 8)) return E8Q_ERR_INVALID_ARG;
+        if (m->ovf_row_ptr && !aligned(m->ovf, 4)) return E8Q_ERR_INVALID_ARG;
+    }
+    int dev;
+    st = ensure_device(&dev);
+    if (st != E8Q_OK) return st;
+    DecodeRowsParams p;
+    p.idx = m->idx;
+    p.scale = m->scale;
+    p.signs = m->signs;
+    p.esc = m->esc;
+    p.esc_rp = m->esc_row_ptr;
+    p.ovf = m->ovf;
+    p.ovf_rp = m->ovf_row_ptr;
+    p.ids = ids;
+    p.out = out;
+    const int64_t most_records = (int64_t{1} << 32) - 1;
+    p.esc_n = static_cast<uint32_t>(m->esc_row_ptr ? std::min(m->esc_count, most_records) : 0);
+    p.ovf_n = static_cast<uint32_t>(m->ovf_row_ptr ? std::min(m->ovf_count, most_records) : 0);
+    p.group_base = static_cast<uint32_t>(m->group_base);
+    p.first_row = first_row;
+    p.n = n;
+    p.alpha = alpha;
+    p.sqrt_b = std::sqrt(static_cast<float>(1 << logb));
+    p.rows = static_cast<int32_t>(m->rows);
+    p.cols = static_cast<int32_t>(m->cols);
+    p.logb = logb;
+    p.nwin = (p.cols + 2047) / 2048;
+    p.id64 = id_type == E8Q_I64 ? 1 : 0;
+    p.idx_copy = (p.cols % 64 == 0 && aligned(p.idx, 16)) ? 16 : (p.cols % 16 == 0 && aligned(p.idx, 4)) ? 4 : 0;
+    const int64_t ctas = (n * p.nwin + kDrWarps - 1) / kDrWarps, most = int64_t{kDrCtas} * g_sms[dev];
+    const int grid = static_cast<int>(ctas < most ? ctas : most);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool orig = basis == E8Q_DEQUANT_ORIGINAL, f32 = out_dtype == E8Q_F32, full = p.cols % 2048 == 0;
+    const size_t smem = dr_smem_bytes(orig, p.cols);
+    auto launch = [&](auto kernel) {
+        kernel<<<grid, kDrThreads, smem, s>>>(p);
+        return cuda_ok(cudaGetLastError());
+    };
+    if (orig && f32) return full ? launch(k_decode_rows<true, true, true>) : launch(k_decode_rows<true, true, false>);
+    if (orig) return full ? launch(k_decode_rows<true, false, true>) : launch(k_decode_rows<true, false, false>);
+    if (f32) return full ? launch(k_decode_rows<false, true, true>) : launch(k_decode_rows<false, true, false>);
+    return full ? launch(k_decode_rows<false, false, true>) : launch(k_decode_rows<false, false, false>);
+}
+
+size_t e8q_rows_backward_workspace_bytes(int64_t n, int64_t cols) {
+    if (n < 0 || n > kMaxIds || !valid_cols(cols) || cols > kMaxCols) return 256;
+    return rb_plan(n, cols).total;
+}
+
+e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const void* ids, int32_t id_type, int64_t n,
+                             int64_t first_row, float alpha, int32_t accumulate, void* grad_latent,
+                             int32_t latent_dtype, int64_t rows, int64_t cols, void* ws, size_t ws_bytes,
+                             e8q_stream stream) {
+    if (n < 0 || rows < 0 || !valid_cols(cols) || !valid_dtype(grad_dtype) || !valid_dtype(latent_dtype) ||
+        !valid_id_type(id_type) || !std::isfinite(alpha) || (accumulate != 0 && accumulate != 1))
+        return E8Q_ERR_INVALID_ARG;
+    if (cols > kMaxCols || rows > (int64_t{1} << 30) || n > kMaxIds) return E8Q_ERR_UNSUPPORTED;
+    if (rows == 0 || (n == 0 && accumulate)) return E8Q_OK;
+    if (!grad_latent || !aligned(grad_latent, 16)) return E8Q_ERR_INVALID_ARG;
+    const size_t lat_bytes = static_cast<size_t>(rows) * cols * dtype_bytes(latent_dtype);
+    if (n > 0) {
+        if (!grad_out || !aligned(grad_out, 16) || !ids || !aligned(ids, id_bytes(id_type))) return E8Q_ERR_INVALID_ARG;
+        if (overlap(grad_out, static_cast<size_t>(n) * cols * dtype_bytes(grad_dtype), grad_latent, lat_bytes) ||
+            overlap(ids, static_cast<size_t>(n) * id_bytes(id_type), grad_latent, lat_bytes))
+            return E8Q_ERR_INVALID_ARG;
+    }
+    const RbPlan pl = rb_plan(n, cols);
+    if (n > kRbDirectMax && (!ws || ws_bytes < pl.total || !aligned(ws, 256))) return E8Q_ERR_WORKSPACE;
+    int dev;
+    e8q_status st = ensure_device(&dev);
+    if (st != E8Q_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (n == 0) return cuda_ok(cudaMemsetAsync(grad_latent, 0, lat_bytes, s));
+    unsigned char* w = static_cast<unsigned char*>(ws);
+
+    RbSumParams q = {};
+    q.ids.ids = ids;
+    q.ids.first_row = first_row;
+    q.ids.id64 = id_type == E8Q_I64 ? 1 : 0;
+    q.ids.rows = static_cast<int32_t>(rows);
+    q.grad = grad_out;
+    q.latent = grad_latent;
+    q.n = n;
+    q.alpha = alpha;
+    q.cols = static_cast<int32_t>(cols);
+    q.slices = static_cast<int32_t>(pl.slices);
+    q.chunk = static_cast<int32_t>(pl.chunk);
+    q.accumulate = accumulate;
+    const int64_t zero_ctas = accumulate ? 0 : (rows + kRbZeroRows - 1) / kRbZeroRows;
+    const bool gf = grad_dtype == E8Q_F32, lf = latent_dtype == E8Q_F32;
+    if (n <= kRbDirectMax) {
+        q.sum_ctas = n * pl.slices;
+        const unsigned grid = static_cast<unsigned>(q.sum_ctas + zero_ctas);
+        if (gf && lf) k_rb_direct<true, true><<<grid, kRbThreads, 0, s>>>(q);
+        else if (gf) k_rb_direct<true, false><<<grid, kRbThreads, 0, s>>>(q);
+        else if (lf) k_rb_direct<false, true><<<grid, kRbThreads, 0, s>>>(q);
+        else k_rb_direct<false, false><<<grid, kRbThreads, 0, s>>>(q);
+        return cuda_ok(cudaGetLastError());
+    }
+
+    int at = 0;
+    if (n <= kRbRankMax) {
+        RbRankParams r;
+        r.ids = q.ids;
+        r.n = static_cast<int32_t>(n);
+        r.keys = reinterpret_cast<int32_t*>(w + pl.keys[0]);
+        r.order = reinterpret_cast<int32_t*>(w + pl.order[0]);
+        k_rb_rank<<<static_cast<unsigned>((n + kRbRankKeys - 1) / kRbRankKeys), kRbRankThreads, 0, s>>>(r);
+        st = cuda_ok(cudaGetLastError());
+    } else {
+        int bits = 1;
+        while ((int64_t{1} << bits) <= rows) ++bits;  // keys 0 .. rows
+        const int passes = (bits + kRbDigitBits - 1) / kRbDigitBits, digit = (bits + passes - 1) / passes;
+        RbRadixParams r;
+        r.ids = q.ids;
+        r.n = n;
+        r.hist = reinterpret_cast<uint32_t*>(w + pl.hist);
+        r.mask = (1 << digit) - 1;
+        const int grid = static_cast<int>(pl.radix_ctas);
+        for (int i = 0; i < passes && st == E8Q_OK; ++i) {
+            at = i & 1;
+            r.shift = i * digit;
+            r.keys_in = i ? reinterpret_cast<const int32_t*>(w + pl.keys[at ^ 1]) : nullptr;
+            r.order_in = i ? reinterpret_cast<const int32_t*>(w + pl.order[at ^ 1]) : nullptr;
+            r.keys = reinterpret_cast<int32_t*>(w + pl.keys[at]);
+            r.order = reinterpret_cast<int32_t*>(w + pl.order[at]);
+            if (i == 0) {
+                k_rb_hist<<<grid, 256, 0, s>>>(r);
+                st = cuda_ok(cudaGetLastError());
+            } else {
+                st = launch_pdl(k_rb_hist, grid, 256, 0, s, r);
+            }
+            if (st == E8Q_OK) st = launch_pdl(k_rb_scatter, grid, 256, 0, s, r);
+        }
+    }
+    if (st != E8Q_OK) return st;
+    q.keys = reinterpret_cast<const int32_t*>(w + pl.keys[at]);
+    q.order = reinterpret_cast<const int32_t*>(w + pl.order[at]);
+    q.part = reinterpret_cast<float*>(w + pl.part);
+    q.sum_ctas = pl.chunks * pl.slices;
+    const int64_t grid = q.sum_ctas + zero_ctas;
+    if (grid > 0x7FFFFFFF) return E8Q_ERR_UNSUPPORTED;
+    if (gf && lf) st = launch_pdl(k_rb_sum<true, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
+    else if (gf) st = launch_pdl(k_rb_sum<true, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
+    else if (lf) st = launch_pdl(k_rb_sum<false, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
+    else st = launch_pdl(k_rb_sum<false, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
+    if (st != E8Q_OK || pl.chunks == 1) return st;
+    const int64_t jgrid = (pl.chunks - 1) * ((cols + kRbJoinCols - 1) / kRbJoinCols);
+    if (jgrid > 0x7FFFFFFF) return E8Q_ERR_UNSUPPORTED;
+    return lf ? launch_pdl(k_rb_join<true>, static_cast<int>(jgrid), kRbJoinThreads, 0, s, q)
+              : launch_pdl(k_rb_join<false>, static_cast<int>(jgrid), kRbJoinThreads, 0, s, q);
 }
 
 }  // extern "C"

@@ -7,6 +7,7 @@ raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass, field
@@ -20,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libe8q.so")
 
 E8Q_OK = 0
 E8Q_F32, E8Q_BF16 = 0, 1
+E8Q_I32, E8Q_I64 = 0, 1
 DEQUANT = {"none": 0, "rotated": 1, "original": 2}
 
 ESC_DTYPE = np.dtype([("group", "<u4"), ("core", "<u2"), ("root", "u1"), ("reserved", "u1")])
@@ -91,6 +93,13 @@ def lib():
         L.e8q_gemm_workspace_bytes.restype = sz
         L.e8q_dequant_gemm.argtypes = [ctypes.POINTER(EncodedC), vp, i32, vp, vp, sz, vp]
         L.e8q_dequant_gemm.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        L.e8q_decode_rows.argtypes = [ctypes.POINTER(EncodedC), i32, vp, i32, i64, i64, f32, vp, i32, vp]
+        L.e8q_decode_rows.restype = ctypes.c_int
+        L.e8q_rows_backward_workspace_bytes.argtypes = [i64, i64]
+        L.e8q_rows_backward_workspace_bytes.restype = sz
+        L.e8q_rows_backward.argtypes = [vp, i32, vp, i32, i64, i64, f32, i32, vp, i32, i64, i64, vp, sz, vp]
+        L.e8q_rows_backward.restype = ctypes.c_int
         L.e8q_ste_backward.argtypes = [vp, vp, i64, vp]
         L.e8q_ste_backward.restype = ctypes.c_int
         _lib = L
@@ -116,6 +125,42 @@ def _require_cuda(t: torch.Tensor, name: str):
         raise E8qError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise E8qError(f"{name} must be contiguous")
+
+
+_DTYPES = {torch.float32: E8Q_F32, torch.bfloat16: E8Q_BF16}
+_ID_TYPES = {torch.int32: E8Q_I32, torch.int64: E8Q_I64}
+
+
+def _require(t: torch.Tensor, name: str, shape, dtypes, device: torch.device):
+    """A contiguous CUDA tensor of this shape and of one of these types, on this device."""
+    _require_cuda(t, name)
+    if t.device != device:
+        raise E8qError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise E8qError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, got {str(t.dtype)[6:]}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise E8qError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _call(what: str, device: torch.device, stream, *args):
+    """One library call on the device of its tensors: on `stream`, or on that
+    device's current stream."""
+    fn = getattr(lib(), what)
+    if device.index == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream()
+        rc = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream()
+            rc = fn(*args, s.cuda_stream)
+    if rc != E8Q_OK:
+        _check(rc, what)
+
+
+def _allocating_on(stream):
+    """Context in which new tensors belong to the stream that a call runs on
+    (torch's allocator hands memory out per stream)."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def core_table() -> np.ndarray:
@@ -160,9 +205,13 @@ class Encoded:
     ovf_count: int = 0
 
     def c(self) -> EncodedC:
-        return EncodedC(_ptr(self.idx), _ptr(self.scale), _ptr(self.signs), _ptr(self.esc), _ptr(self.esc_row_ptr),
-                        _ptr(self.ovf), _ptr(self.ovf_row_ptr), self.esc_count, self.ovf_count, self.rows, self.cols,
-                        self.group_base, self.rht_block, 0)
+        # an empty record buffer has no address: its row pointers go with it
+        esc = self.esc if self.esc is not None and self.esc.numel() else None
+        ovf = self.ovf if self.ovf is not None and self.ovf.numel() else None
+        return EncodedC(_ptr(self.idx), _ptr(self.scale), _ptr(self.signs), _ptr(esc),
+                        _ptr(self.esc_row_ptr) if esc is not None else None, _ptr(ovf),
+                        _ptr(self.ovf_row_ptr) if ovf is not None else None, self.esc_count, self.ovf_count, self.rows,
+                        self.cols, self.group_base, self.rht_block, 0)
 
 
 @dataclass
@@ -353,6 +402,80 @@ def e8q_ste_backward(grad_dequant: torch.Tensor, grad_latent: Optional[torch.Ten
     _check(lib().e8q_ste_backward(_ptr(grad_dequant), _ptr(out), grad_dequant.numel(), _stream_handle(stream)),
            "e8q_ste_backward")
     return out
+
+
+def e8q_decode_rows(m: Encoded, ids: torch.Tensor, basis: str = "original", alpha: float = 1.0, first_row: int = 0,
+                    out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """alpha * w~[ids - first_row]: chosen rows of an encoded matrix (an
+    embedding table in the 2-bit form), of shape ids.shape + (cols,) in bf16
+    or fp32.  ids: int32 or int64, any shape; ids outside the matrix give
+    zeros.  out (if given) has that shape and sets the output type."""
+    device = m.idx.device
+    _require(ids, "ids", None, _ID_TYPES, device)
+    if basis not in ("rotated", "original"):
+        raise E8qError("basis must be 'rotated' or 'original'")
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise E8qError("out_dtype must be float32 or bfloat16")
+        with _allocating_on(stream):
+            out = torch.empty(ids.shape + (m.cols,), dtype=out_dtype, device=device)
+    else:
+        _require(out, "out", ids.shape + (m.cols,), _DTYPES, device)
+    _call("e8q_decode_rows", device, stream, ctypes.byref(m.c()), DEQUANT[basis], ids.data_ptr(), _ID_TYPES[ids.dtype],
+          ids.numel(), int(first_row), float(alpha), out.data_ptr(), _DTYPES[out.dtype])
+    return out
+
+
+class RowsBackward:
+    """Pre-allocated workspace for the gradient of e8q_decode_rows: latent
+    rows [rows][cols] from up to max_ids output rows.  The object may be
+    used by one call at a time: calls that may overlap on the GPU (other
+    streams, graphs replayed side by side) need an object each."""
+
+    def __init__(self, rows: int, cols: int, max_ids: int, grad_dtype=torch.bfloat16, latent_dtype=torch.bfloat16,
+                 device=None):
+        if grad_dtype not in _DTYPES or latent_dtype not in _DTYPES:
+            raise E8qError("gradients must be float32 or bfloat16")
+        self.rows, self.cols, self.max_ids = int(rows), int(cols), int(max_ids)
+        self.grad_dtype, self.latent_dtype = grad_dtype, latent_dtype
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        ws = lib().e8q_rows_backward_workspace_bytes(self.max_ids, self.cols)
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
+        self.grad_latent = None
+
+    def __call__(self, grad_out: torch.Tensor, ids: torch.Tensor, grad_latent: Optional[torch.Tensor] = None,
+                 alpha: float = 1.0, first_row: int = 0, accumulate: bool = False, stream=None) -> torch.Tensor:
+        """grad_latent (+)= alpha * sums of grad_out [..., cols] over equal
+        ids; grad_latent None: a buffer of this object (not with accumulate)."""
+        n = ids.numel()
+        _require(ids, "ids", None, _ID_TYPES, self.device)
+        _require(grad_out, "grad_out", ids.shape + (self.cols,), (self.grad_dtype,), self.device)
+        if n > self.max_ids:
+            raise E8qError(f"{n} ids given to an object for {self.max_ids}")
+        if grad_latent is None:
+            if accumulate:
+                raise E8qError("accumulate needs grad_latent")
+            if self.grad_latent is None:
+                self.grad_latent = torch.empty((self.rows, self.cols), dtype=self.latent_dtype, device=self.device)
+            grad_latent = self.grad_latent
+        else:
+            _require(grad_latent, "grad_latent", (self.rows, self.cols), (self.latent_dtype,), self.device)
+        _call("e8q_rows_backward", self.device, stream, grad_out.data_ptr(), _DTYPES[self.grad_dtype], ids.data_ptr(),
+              _ID_TYPES[ids.dtype], n, int(first_row), float(alpha), 1 if accumulate else 0, grad_latent.data_ptr(),
+              _DTYPES[self.latent_dtype], self.rows, self.cols, self.workspace.data_ptr(), self.workspace.numel())
+        return grad_latent
+
+
+def e8q_rows_backward(grad_out: torch.Tensor, ids: torch.Tensor, rows: int, alpha: float = 1.0, first_row: int = 0,
+                      grad_latent: Optional[torch.Tensor] = None, accumulate: bool = False,
+                      latent_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """One-shot RowsBackward (allocates its workspace and, unless given,
+    grad_latent [rows][cols])."""
+    _require_cuda(grad_out, "grad_out")
+    latent_dtype = latent_dtype if grad_latent is None else grad_latent.dtype
+    with _allocating_on(stream):
+        op = RowsBackward(rows, grad_out.shape[-1], ids.numel(), grad_out.dtype, latent_dtype, grad_out.device)
+        return op(grad_out, ids, grad_latent, alpha, first_row, accumulate, stream)
 
 
 class Gemv:

@@ -76,6 +76,7 @@ typedef enum {
 } e8q_status;
 
 typedef enum { E8Q_F32 = 0, E8Q_BF16 = 1 } e8q_dtype;
+typedef enum { E8Q_I32 = 0, E8Q_I64 = 1 } e8q_id_type; /* row / token ids */
 
 typedef enum {
     E8Q_DEQUANT_NONE = 0,
@@ -346,6 +347,68 @@ e8q_status e8q_dequant_gemm(const e8q_encoded* m /* host */, const void* x_bf16,
  * misaligned pointers with n > 0, partially overlapping buffers), CUDA.
  */
 e8q_status e8q_ste_backward(const void* grad_dequant, void* grad_latent, int64_t n, e8q_stream stream);
+
+/*
+ * Chosen rows of an encoded matrix, decoded and scaled: the lookup of an
+ * embedding table held in the 2-bit form (abstract: core encoding and sparse
+ * extension keep the lattice points exactly),
+ *   out[t] = alpha * w~[id_t - first_row],   t = 0 .. n-1,
+ * with w~ as e8q_decode gives it in the same basis, rounded once to the
+ * output type.  An id outside [first_row, first_row + m->rows) gives a row
+ * of zeros, so that padding ids read as 0 and the lookups of row shards of
+ * one table add up to the lookup in the whole table.
+ *
+ * ids: [n] of id_type (e8q_id_type), aligned to their size; the same id may
+ * occur any number of times.  out: [n][cols] bf16 or fp32 (out_dtype),
+ * 16-byte aligned.  0 <= n <= 2^30.  alpha finite.  m->signs (original
+ * basis) 8-byte aligned, m->esc 8-byte, m->ovf 4-byte aligned.  Records as
+ * for e8q_decode; records outside their row are ignored.
+ *
+ * Arithmetic: the Hadamard transform of the original basis is formed on the
+ * integer coordinates (exact up to 2^24), then multiplied by the fp32 value
+ * (alpha s_r) / sqrt(B); the rotated basis rounds the exact product of the
+ * fp32 value alpha s_r and the point.  With alpha = 1 and bf16 the rows are
+ * those of e8q_decode, bit for bit, wherever the transform stays below 2^24.
+ * Needs no workspace.  Asynchronous on `stream`; errors: INVALID_ARG,
+ * UNSUPPORTED (n > 2^30, cols > 16384, group ids past 2^32), CUDA.
+ */
+e8q_status e8q_decode_rows(const e8q_encoded* m /* host */, int32_t basis, const void* ids, int32_t id_type,
+                           int64_t n, int64_t first_row, float alpha, void* out, int32_t out_dtype,
+                           e8q_stream stream);
+
+/*
+ * Workspace bytes e8q_rows_backward needs for n ids or fewer and this width
+ * (the same on every device; 256 for arguments the call would reject).
+ * Needs no GPU.
+ */
+size_t e8q_rows_backward_workspace_bytes(int64_t n, int64_t cols);
+
+/*
+ * Identity-STE backward of e8q_decode_rows in the original basis: the
+ * gradient of the latent rows,
+ *   grad_latent[r] = alpha * sum over t with id_t - first_row = r of grad_out[t],
+ * or, with accumulate = 1, grad_latent[r] + that sum.  Ids outside
+ * [first_row, first_row + rows) are left out.  With accumulate = 0 every row
+ * is written (zeros where no id points); with accumulate = 1 rows without an
+ * id are not touched.
+ *
+ * grad_out: [n][cols] bf16 or fp32 (grad_dtype); grad_latent: [rows][cols]
+ * bf16 or fp32 (latent_dtype); both 16-byte aligned, cols a multiple of 8
+ * up to 16384; no buffer may overlap grad_latent.  ids as for
+ * e8q_decode_rows.  ws: device memory of at least
+ * e8q_rows_backward_workspace_bytes(n, cols) bytes, 256-byte aligned, owned
+ * by the caller, overwritten (not read for n <= 128: may be NULL then); two
+ * calls that may run at the same time need one each.
+ *
+ * Arithmetic: fp32 sums, rounded once to latent_dtype.  The order of the sum
+ * follows from the ids and the shapes alone (no atomics), so repeated calls
+ * give the same bits on any device.  Asynchronous on `stream`; errors:
+ * INVALID_ARG, UNSUPPORTED (cols > 16384, n or rows > 2^30), WORKSPACE, CUDA.
+ */
+e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const void* ids, int32_t id_type, int64_t n,
+                             int64_t first_row, float alpha, int32_t accumulate, void* grad_latent,
+                             int32_t latent_dtype, int64_t rows, int64_t cols, void* ws, size_t ws_bytes,
+                             e8q_stream stream);
 
 /*
  * Project + encode without allocating anything: the same computation and
