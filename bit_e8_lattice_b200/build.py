@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libe8q.so")
-SOURCES = ["e8q.cu", "tables.cpp"]
+SOURCES = ["e8q.cu", "lora.cu", "tables.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -24,7 +24,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return SO
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = SO + ".tmp"
-    cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-O3",
+    cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-t", "0", "-Xcompiler", "-fPIC,-O3",
            "-I", os.path.join(ROOT, "include"), "-o", tmp]
     if verbose:
         cmd += ["-Xptxas", "-v"]

@@ -17,6 +17,7 @@
 #include "encode_fast.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
+#include "host.cuh"
 #include "rows_backward.cuh"
 #include "ste.cuh"
 #include "tables.h"
@@ -28,8 +29,6 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 bool g_ready[kMaxDevices];
 int g_sms[kMaxDevices];
-
-e8q_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? E8Q_OK : E8Q_ERR_CUDA; }
 
 e8q_status ensure_device(int* dev_out) {
     int dev = 0;
@@ -143,26 +142,6 @@ e8q_status ensure_device(int* dev_out) {
     return E8Q_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Launch with programmatic stream serialisation: the kernel may start while
-// the previous kernel on the stream is finishing; it waits for that
-// kernel's results with griddepcontrol.wait.
-template <typename P>
-e8q_status launch_pdl(void (*kernel)(P), int grid, int threads, size_t smem, cudaStream_t s, const P& params) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, params));
-}
-
 // log2 of the effective RHT block, or -1 if invalid
 int resolve_logb(int64_t cols, int32_t block) {
     if (block == 1) return 0;
@@ -178,8 +157,6 @@ int resolve_logb(int64_t cols, int32_t block) {
 }
 
 bool valid_cols(int64_t cols) { return cols >= 8 && cols % 8 == 0; }
-
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // The fast kernel takes bf16 rows whose width is a multiple of 256, with an
 // RHT block of at least 256, and 16-byte aligned index / output buffers.
@@ -282,11 +259,6 @@ bool valid_dtype(int32_t t) { return t == E8Q_F32 || t == E8Q_BF16; }
 bool valid_id_type(int32_t t) { return t == E8Q_I32 || t == E8Q_I64; }
 size_t dtype_bytes(int32_t t) { return t == E8Q_F32 ? 4 : 2; }
 size_t id_bytes(int32_t t) { return t == E8Q_I32 ? 4 : 8; }
-
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bn && y < x + an;
-}
 
 constexpr int64_t kMaxIds = int64_t{1} << 30;
 

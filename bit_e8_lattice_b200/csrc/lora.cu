@@ -1,0 +1,315 @@
+// Entry points of the low-rank adapters (include/e8q.h) over lora.cuh.
+#include "lora.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+#include "host.cuh"
+
+namespace e8q {
+namespace {
+
+constexpr int64_t kFill = 3 * 148;  // CTAs that fill the SMs; a constant, so that the order of the sums is the same on any device
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct LrGeom {
+    int tile, mt;            // tokens a tile; 16-row tiles of the rank in a k_lr_down CTA
+    int64_t tiles;           // most tiles
+    int64_t zparts;          // rank parts of k_lr_down
+    int64_t unit, units, parts;  // tokens a unit, most units, most partial sums (backward)
+};
+
+LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
+    LrGeom g;
+    g.tile = tokens <= kLrSmallTokens ? kLrSmallTile : kLrTile;
+    // every group (the tokens without an adapter are one) adds at most one tile that is not full
+    g.tiles = std::min(tokens, ceil_div(tokens, g.tile) + std::min<int64_t>(tokens, int64_t{a.n} + 1));
+    g.mt = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
+    g.zparts = ceil_div(a.rank, 64);
+    const int64_t along = ceil_div(a.rows, kLrGradCols) + ceil_div(a.cols, kLrGradCols);
+    g.unit = ceil_div(ceil_div(tokens, std::max<int64_t>(1, kFill / along)), 64) * 64;
+    g.units = ceil_div(tokens, g.unit) + std::min<int64_t>(tokens, a.n);
+    g.parts = 2 * ceil_div(tokens, g.unit);  // an adapter of several units has all but one full
+    return g;
+}
+
+// columns a CTA of k_lr_down: at most 4,096 (a warp's sum then has at most
+// 64 MMAs of 16 columns), fewer where there are few tiles
+int64_t down_columns(const LrGeom& g, int64_t cols) {
+    const int64_t least = ceil_div(cols, 4096), most = ceil_div(cols, 256);
+    const int64_t splits = std::min(most, std::max(least, ceil_div(kFill, g.tiles * g.zparts)));
+    return ceil_div(ceil_div(cols, splits), 256) * 256;
+}
+
+struct LrWs {
+    size_t head, order, tiles, units, unit_base, part, parts, grads, total;
+};
+
+LrWs workspace(const e8q_adapters& a, int64_t tokens, const LrGeom& g, bool backward) {
+    LrWs w = {};
+    size_t at = 0;
+    auto take = [&at](size_t bytes) {
+        const size_t o = at;
+        at += align256(bytes);
+        return o;
+    };
+    w.head = take(16);
+    w.order = take(static_cast<size_t>(tokens) * 4);
+    w.tiles = take(static_cast<size_t>(g.tiles) * sizeof(LrTile));
+    w.units = take(static_cast<size_t>(g.units) * sizeof(LrTile));
+    w.unit_base = take(static_cast<size_t>(a.n) * 8);
+    const int64_t cols = backward ? a.rows : a.cols;
+    const int64_t splits = ceil_div(cols, down_columns(g, cols));
+    w.part = take(static_cast<size_t>(splits) * tokens * a.rank * 4);
+    if (backward) {
+        w.parts = take(static_cast<size_t>(4) * tokens * a.rank * 2);
+        w.grads = take(static_cast<size_t>(g.parts) * (a.rows + a.cols) * a.rank * 4);
+    }
+    w.total = at;
+    return w;
+}
+
+e8q_status check(const e8q_adapters* a, int64_t tokens) {
+    if (!a || tokens < 0 || a->n < 0 || a->rows <= 0 || a->cols <= 0 || a->rank <= 0) return E8Q_ERR_INVALID_ARG;
+    if (a->rows % 8 != 0 || a->cols % 8 != 0 || a->rank % 8 != 0) return E8Q_ERR_INVALID_ARG;
+    if (a->rows > kLrMaxWidth || a->cols > kLrMaxWidth || a->rank > kLrMaxRank || a->n > kLrMaxAdapters ||
+        tokens > kLrMaxTokens)
+        return E8Q_ERR_UNSUPPORTED;
+    if (a->n > 0 && (!a->a || !a->b || !a->scale || !aligned(a->a, 16) || !aligned(a->b, 16) || !aligned(a->scale, 4)))
+        return E8Q_ERR_INVALID_ARG;
+    return E8Q_OK;
+}
+
+size_t plan_smem(int n) { return static_cast<size_t>(n + 2) * 16 + static_cast<size_t>(n + 1) * 64; }
+
+template <bool kSmall, bool kTrans>
+e8q_status down_attributes() {
+    cudaError_t e = cudaFuncSetAttribute(k_lr_down<1, kSmall, kTrans>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(lr_down_smem(1, kSmall, kTrans)));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_lr_down<2, kSmall, kTrans>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(lr_down_smem(2, kSmall, kTrans)));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_lr_down<4, kSmall, kTrans>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(lr_down_smem(4, kSmall, kTrans)));
+    return cuda_ok(e);
+}
+
+template <int NT>
+e8q_status grad_attributes() {
+    return cuda_ok(cudaFuncSetAttribute(k_lr_grad<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(lr_grad_smem(NT))));
+}
+
+// Shared-memory limits of the kernels, once per device.
+e8q_status ensure_lora() {
+    static std::mutex mu;
+    static bool ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return E8Q_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return E8Q_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> lock(mu);
+    if (ready[dev]) return E8Q_OK;
+    e8q_status st = cuda_ok(cudaFuncSetAttribute(k_lr_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(plan_smem(kLrMaxAdapters))));
+    if (st == E8Q_OK) st = down_attributes<false, false>();
+    if (st == E8Q_OK) st = down_attributes<false, true>();
+    if (st == E8Q_OK) st = down_attributes<true, false>();
+    if (st == E8Q_OK) st = down_attributes<true, true>();
+    if (st == E8Q_OK) st = grad_attributes<2>();
+    if (st == E8Q_OK) st = grad_attributes<4>();
+    if (st == E8Q_OK) st = grad_attributes<8>();
+    if (st == E8Q_OK) st = grad_attributes<16>();
+    ready[dev] = st == E8Q_OK;
+    return st;
+}
+
+e8q_status launch_plan(const e8q_adapters& a, const int32_t* slots, int64_t tokens, const LrGeom& g, const LrWs& l,
+                       unsigned char* w, cudaStream_t s) {
+    LrPlanParams p;
+    p.slots = slots;
+    p.tokens = static_cast<int32_t>(tokens);
+    p.n = a.n;
+    p.tile = g.tile;
+    p.unit = static_cast<int32_t>(g.unit);
+    p.head = reinterpret_cast<int32_t*>(w + l.head);
+    p.order = reinterpret_cast<int32_t*>(w + l.order);
+    p.tiles = reinterpret_cast<LrTile*>(w + l.tiles);
+    p.units = reinterpret_cast<LrTile*>(w + l.units);
+    p.unit_base = reinterpret_cast<int32_t*>(w + l.unit_base);
+    k_lr_plan<<<1, kLrPlanThreads, plan_smem(a.n), s>>>(p);
+    return cuda_ok(cudaGetLastError());
+}
+
+template <bool kTrans>
+e8q_status launch_down(const e8q_adapters& a, const void* z, const void* weights, int64_t cols, int64_t tokens,
+                       const LrGeom& g, const LrWs& l, unsigned char* w, cudaStream_t s) {
+    LrDownParams p;
+    p.head = reinterpret_cast<const int32_t*>(w + l.head);
+    p.order = reinterpret_cast<const int32_t*>(w + l.order);
+    p.tiles = reinterpret_cast<const LrTile*>(w + l.tiles);
+    p.z = static_cast<const uint16_t*>(z);
+    p.w = static_cast<const uint16_t*>(weights);
+    p.part = reinterpret_cast<float*>(w + l.part);
+    p.tokens = static_cast<int32_t>(tokens);
+    p.cols = static_cast<int32_t>(cols);
+    p.rank = a.rank;
+    p.per = static_cast<int32_t>(down_columns(g, cols));
+    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.per)), static_cast<unsigned>(g.zparts));
+    const bool small = g.tile == kLrSmallTile;
+    const size_t smem = lr_down_smem(g.mt, small, kTrans);
+    if (small) {
+        if (g.mt == 1) return launch_pdl(k_lr_down<1, true, kTrans>, grid, kLrDownThreads, smem, s, p);
+        if (g.mt == 2) return launch_pdl(k_lr_down<2, true, kTrans>, grid, kLrDownThreads, smem, s, p);
+        return launch_pdl(k_lr_down<4, true, kTrans>, grid, kLrDownThreads, smem, s, p);
+    }
+    if (g.mt == 1) return launch_pdl(k_lr_down<1, false, kTrans>, grid, kLrDownThreads, smem, s, p);
+    if (g.mt == 2) return launch_pdl(k_lr_down<2, false, kTrans>, grid, kLrDownThreads, smem, s, p);
+    return launch_pdl(k_lr_down<4, false, kTrans>, grid, kLrDownThreads, smem, s, p);
+}
+
+template <bool kTrans>
+e8q_status launch_up(const e8q_adapters& a, const void* weights, const void* base, void* out, float* sum, int64_t cols,
+                     int64_t sum_cols, int64_t tokens, const LrGeom& g, const LrWs& l, unsigned char* w, cudaStream_t s) {
+    LrUpParams p;
+    p.head = reinterpret_cast<const int32_t*>(w + l.head);
+    p.order = reinterpret_cast<const int32_t*>(w + l.order);
+    p.tiles = reinterpret_cast<const LrTile*>(w + l.tiles);
+    p.part = reinterpret_cast<const float*>(w + l.part);
+    p.scale = a.scale;
+    p.w = static_cast<const uint16_t*>(weights);
+    p.base = static_cast<const uint16_t*>(base);
+    p.out = static_cast<uint16_t*>(out);
+    p.sum = sum;
+    p.tokens = static_cast<int32_t>(tokens);
+    p.cols = static_cast<int32_t>(cols);
+    p.rank = a.rank;
+    p.splits = static_cast<int32_t>(ceil_div(sum_cols, down_columns(g, sum_cols)));
+    // long ranges share the factors' preparation, short ones fill the GPU
+    p.range = g.tiles * ceil_div(cols, 512) >= kFill ? 512 : 128;
+    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.range)));
+    return launch_pdl(k_lr_up<kTrans>, grid, kLrUpThreads, lr_up_smem(a.rank), s, p);
+}
+
+}  // namespace
+}  // namespace e8q
+
+using namespace e8q;
+
+extern "C" {
+
+size_t e8q_lora_workspace_bytes(const e8q_adapters* a, int64_t tokens, int32_t backward) {
+    if (check(a, tokens) != E8Q_OK || tokens == 0) return 256;
+    return workspace(*a, tokens, geometry(*a, tokens), backward != 0).total;
+}
+
+e8q_status e8q_lora(const e8q_adapters* a, const void* x, const int32_t* slots, int64_t tokens, const void* base,
+                    void* y, float* u, void* ws, size_t ws_bytes, e8q_stream stream) {
+    e8q_status st = check(a, tokens);
+    if (st != E8Q_OK || tokens == 0) return st;
+    if (!x || !slots || !y || !aligned(x, 16) || !aligned(slots, 4) || !aligned(y, 16) || !aligned(base, 16) || !aligned(u, 16))
+        return E8Q_ERR_INVALID_ARG;
+    const size_t xb = static_cast<size_t>(tokens) * a->cols * 2, yb = static_cast<size_t>(tokens) * a->rows * 2;
+    const size_t ub = static_cast<size_t>(tokens) * a->rank * 4, sb = static_cast<size_t>(tokens) * 4;
+    if (overlap(x, xb, y, yb) || overlap(slots, sb, y, yb) || (base && base != y && overlap(base, yb, y, yb)))
+        return E8Q_ERR_INVALID_ARG;
+    if (u && (overlap(u, ub, x, xb) || overlap(u, ub, y, yb) || overlap(u, ub, slots, sb) || (base && overlap(u, ub, base, yb))))
+        return E8Q_ERR_INVALID_ARG;
+    const LrGeom g = geometry(*a, tokens);
+    const LrWs l = workspace(*a, tokens, g, false);
+    if (!ws || ws_bytes < l.total || !aligned(ws, 256)) return E8Q_ERR_WORKSPACE;
+    st = ensure_lora();
+    if (st != E8Q_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    unsigned char* w = static_cast<unsigned char*>(ws);
+    st = launch_plan(*a, slots, tokens, g, l, w, s);
+    if (st == E8Q_OK) st = launch_down<false>(*a, x, a->a, a->cols, tokens, g, l, w, s);
+    if (st == E8Q_OK) st = launch_up<false>(*a, a->b, base, y, u, a->rows, a->cols, tokens, g, l, w, s);
+    return st;
+}
+
+e8q_status e8q_lora_backward(const e8q_adapters* a, const void* grad_y, const void* x, const float* u,
+                             const int32_t* slots, int64_t tokens, void* grad_a, void* grad_b, const void* grad_x_base,
+                             void* grad_x, void* ws, size_t ws_bytes, e8q_stream stream) {
+    e8q_status st = check(a, tokens);
+    if (st != E8Q_OK) return st;
+    const size_t ab = static_cast<size_t>(a->n) * a->rank * a->cols * 2, bb = static_cast<size_t>(a->n) * a->rank * a->rows * 2;
+    if (a->n > 0 && (!grad_a || !grad_b || !aligned(grad_a, 16) || !aligned(grad_b, 16))) return E8Q_ERR_INVALID_ARG;
+    if (a->n > 0 && overlap(grad_a, ab, grad_b, bb)) return E8Q_ERR_INVALID_ARG;
+    if (tokens > 0) {
+        if (!grad_y || !x || !u || !slots || !aligned(grad_y, 16) || !aligned(x, 16) || !aligned(u, 16) ||
+            !aligned(slots, 4) || !aligned(grad_x, 16) || !aligned(grad_x_base, 16) || (grad_x_base && !grad_x))
+            return E8Q_ERR_INVALID_ARG;
+        const size_t xb = static_cast<size_t>(tokens) * a->cols * 2, yb = static_cast<size_t>(tokens) * a->rows * 2;
+        const size_t ub = static_cast<size_t>(tokens) * a->rank * 4, sb = static_cast<size_t>(tokens) * 4;
+        const struct { const void* p; size_t n; } ins[] = {{grad_y, yb}, {x, xb}, {u, ub}, {slots, sb}, {a->a, ab}, {a->b, bb}};
+        for (const auto& i : ins) {
+            if (a->n > 0 && (overlap(i.p, i.n, grad_a, ab) || overlap(i.p, i.n, grad_b, bb))) return E8Q_ERR_INVALID_ARG;
+            if (grad_x && overlap(i.p, i.n, grad_x, xb)) return E8Q_ERR_INVALID_ARG;
+        }
+        if (grad_x && a->n > 0 && (overlap(grad_x, xb, grad_a, ab) || overlap(grad_x, xb, grad_b, bb))) return E8Q_ERR_INVALID_ARG;
+        if (grad_x_base && grad_x_base != grad_x && overlap(grad_x_base, xb, grad_x, xb)) return E8Q_ERR_INVALID_ARG;
+        if (grad_x_base && a->n > 0 && (overlap(grad_x_base, xb, grad_a, ab) || overlap(grad_x_base, xb, grad_b, bb)))
+            return E8Q_ERR_INVALID_ARG;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens == 0) {
+        if (a->n == 0) return E8Q_OK;
+        st = cuda_ok(cudaMemsetAsync(grad_a, 0, ab, s));
+        return st == E8Q_OK ? cuda_ok(cudaMemsetAsync(grad_b, 0, bb, s)) : st;
+    }
+    const LrGeom g = geometry(*a, tokens);
+    const LrWs l = workspace(*a, tokens, g, true);
+    if (!ws || ws_bytes < l.total || !aligned(ws, 256)) return E8Q_ERR_WORKSPACE;
+    st = ensure_lora();
+    if (st != E8Q_OK) return st;
+    unsigned char* w = static_cast<unsigned char*>(ws);
+    st = launch_plan(*a, slots, tokens, g, l, w, s);
+    if (st == E8Q_OK) st = launch_down<true>(*a, grad_y, a->b, a->rows, tokens, g, l, w, s);
+    if (st == E8Q_OK && a->n > 0) {
+        LrSplitParams sp;
+        sp.head = reinterpret_cast<const int32_t*>(w + l.head);
+        sp.order = reinterpret_cast<const int32_t*>(w + l.order);
+        sp.slots = slots;
+        sp.u = u;
+        sp.part = reinterpret_cast<const float*>(w + l.part);
+        sp.scale = a->scale;
+        sp.parts = reinterpret_cast<uint16_t*>(w + l.parts);
+        sp.tokens = static_cast<int32_t>(tokens);
+        sp.rank = a->rank;
+        sp.splits = static_cast<int32_t>(ceil_div(a->rows, down_columns(g, a->rows)));
+        st = launch_pdl(k_lr_split, static_cast<int>(std::min<int64_t>(kFill, ceil_div(tokens * (a->rank / 4), 256))), 256, 0, s, sp);
+        if (st != E8Q_OK) return st;
+        LrGradParams gp;
+        gp.head = sp.head;
+        gp.order = sp.order;
+        gp.units = reinterpret_cast<const LrTile*>(w + l.units);
+        gp.unit_base = reinterpret_cast<const int32_t*>(w + l.unit_base);
+        gp.gy = static_cast<const uint16_t*>(grad_y);
+        gp.x = static_cast<const uint16_t*>(x);
+        gp.parts = sp.parts;
+        gp.part = reinterpret_cast<float*>(w + l.grads);
+        gp.grad_b = static_cast<uint16_t*>(grad_b);
+        gp.grad_a = static_cast<uint16_t*>(grad_a);
+        gp.tokens = sp.tokens;
+        gp.rows = static_cast<int32_t>(a->rows);
+        gp.cols = static_cast<int32_t>(a->cols);
+        gp.rank = a->rank;
+        gp.n = a->n;
+        gp.row_ctas = static_cast<int32_t>(ceil_div(a->rows, kLrGradCols));
+        const dim3 grid(static_cast<unsigned>(g.units), static_cast<unsigned>(gp.row_ctas + ceil_div(a->cols, kLrGradCols)));
+        if (a->rank <= 16) st = launch_pdl(k_lr_grad<2>, grid, kLrGradThreads, lr_grad_smem(2), s, gp);
+        else if (a->rank <= 32) st = launch_pdl(k_lr_grad<4>, grid, kLrGradThreads, lr_grad_smem(4), s, gp);
+        else if (a->rank <= 64) st = launch_pdl(k_lr_grad<8>, grid, kLrGradThreads, lr_grad_smem(8), s, gp);
+        else st = launch_pdl(k_lr_grad<16>, grid, kLrGradThreads, lr_grad_smem(16), s, gp);
+        const int64_t quads = (a->rows + a->cols) * (a->rank / 4);
+        const dim3 jgrid(static_cast<unsigned>(std::min<int64_t>(ceil_div(quads, 256), kFill)), static_cast<unsigned>(a->n));
+        if (st == E8Q_OK) st = launch_pdl(k_lr_join, jgrid, 256, 0, s, gp);
+    }
+    if (st == E8Q_OK && grad_x)
+        st = launch_up<true>(*a, a->a, grad_x_base, grad_x, nullptr, a->cols, a->rows, tokens, g, l, w, s);
+    return st;
+}
+
+}  // extern "C"

@@ -57,6 +57,11 @@ class EncodedC(ctypes.Structure):
                 ("rht_block", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class AdaptersC(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("n", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
 COUNTER_FIELDS = ("n_escape", "n_overflow", "n_nonfinite", "n_dropped", "n_clamped", "err")
 
 _lib = None
@@ -100,6 +105,12 @@ def lib():
         L.e8q_rows_backward_workspace_bytes.restype = sz
         L.e8q_rows_backward.argtypes = [vp, i32, vp, i32, i64, i64, f32, i32, vp, i32, i64, i64, vp, sz, vp]
         L.e8q_rows_backward.restype = ctypes.c_int
+        L.e8q_lora_workspace_bytes.argtypes = [ctypes.POINTER(AdaptersC), i64, i32]
+        L.e8q_lora_workspace_bytes.restype = sz
+        L.e8q_lora.argtypes = [ctypes.POINTER(AdaptersC), vp, vp, i64, vp, vp, vp, vp, sz, vp]
+        L.e8q_lora.restype = ctypes.c_int
+        L.e8q_lora_backward.argtypes = [ctypes.POINTER(AdaptersC), vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+        L.e8q_lora_backward.restype = ctypes.c_int
         L.e8q_ste_backward.argtypes = [vp, vp, i64, vp]
         L.e8q_ste_backward.restype = ctypes.c_int
         _lib = L
@@ -533,3 +544,117 @@ class Gemm:
 
 def e8q_dequant_gemm(m: Encoded, x: torch.Tensor, stream=None) -> torch.Tensor:
     return Gemm(m, x.shape[0])(x, stream=stream).clone()
+
+
+class Lora:
+    """Low-rank adapters beside one projection: y[t] = base[t] +
+    scale[i] B_i (A_i x[t]) with i = slots[t], and the backward pass, for up
+    to max_tokens tokens a call.
+
+    a: bf16 [n][rank][cols], b: bf16 [n][rows][rank], scale: float32 [n] (kept,
+    not copied: a training step may change them in place).  The workspace and
+    the outputs that a call is not given belong to the object and are
+    overwritten by the next call: calls that may overlap on the GPU (other
+    streams, graphs replayed side by side) need an object each."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, max_tokens: int):
+        _require_cuda(a, "a")
+        self.device = a.device
+        if a.dim() != 3 or b.dim() != 3:
+            raise E8qError("a must be [n][rank][cols] and b [n][rows][rank]")
+        self.n, self.rank, self.cols = a.shape
+        self.rows = b.shape[1]
+        _require(a, "a", None, (torch.bfloat16,), self.device)
+        _require(b, "b", (self.n, self.rows, self.rank), (torch.bfloat16,), self.device)
+        _require(scale, "scale", (self.n,), (torch.float32,), self.device)
+        self.a, self.b, self.scale = a, b, scale
+        self.max_tokens = int(max_tokens)
+        if self.max_tokens < 0:
+            raise E8qError("max_tokens must not be negative")
+        self._workspace = [None, None]
+        self._buffers = {}
+
+    def _c(self) -> AdaptersC:
+        return AdaptersC(self.a.data_ptr(), self.b.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.n,
+                         self.rank)
+
+    def _ws(self, ad: AdaptersC, tokens: int, backward: int) -> torch.Tensor:
+        need = lib().e8q_lora_workspace_bytes(ctypes.byref(ad), tokens, backward)
+        ws = self._workspace[backward]
+        if ws is None or ws.numel() < need:
+            need = max(need, lib().e8q_lora_workspace_bytes(ctypes.byref(ad), self.max_tokens, backward))
+            ws = self._workspace[backward] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return ws
+
+    def _out(self, name: str, shape, dtype) -> torch.Tensor:
+        """The object's buffer for this output, its first rows for a smaller call."""
+        t = self._buffers.get(name)
+        if t is None or t.shape[0] < shape[0]:
+            rows = max(self.max_tokens, shape[0]) if name in ("y", "u", "grad_x") else shape[0]
+            t = self._buffers[name] = torch.empty((rows,) + tuple(shape[1:]), dtype=dtype, device=self.device)
+        return t if t.shape[0] == shape[0] else t[: shape[0]]
+
+    def _tokens(self, x: torch.Tensor, slots: torch.Tensor) -> int:
+        _require(slots, "slots", None, (torch.int32,), self.device)
+        tokens = slots.numel()
+        if slots.dim() != 1 or tokens > self.max_tokens:
+            raise E8qError(f"slots must be [tokens] with at most {self.max_tokens} tokens")
+        _require(x, "x", (tokens, self.cols), (torch.bfloat16,), self.device)
+        return tokens
+
+    def __call__(self, x: torch.Tensor, slots: torch.Tensor, base: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None, keep_u: bool = False,
+                 stream=None):
+        """y (bf16 [tokens][rows]); with keep_u or u, (y, u): u = A x, float32
+        [tokens][rank], is what backward needs.  base: the projection's
+        output (None: zeros); out may be base."""
+        tokens = self._tokens(x, slots)
+        if base is not None:
+            _require(base, "base", (tokens, self.rows), (torch.bfloat16,), self.device)
+        ad = self._c()
+        with _allocating_on(stream):
+            if out is None:
+                out = self._out("y", (tokens, self.rows), torch.bfloat16)
+            else:
+                _require(out, "out", (tokens, self.rows), (torch.bfloat16,), self.device)
+            if u is None and keep_u:
+                u = self._out("u", (tokens, self.rank), torch.float32)
+            elif u is not None:
+                _require(u, "u", (tokens, self.rank), (torch.float32,), self.device)
+            ws = self._ws(ad, tokens, 0)
+        _call("e8q_lora", self.device, stream, ctypes.byref(ad), x.data_ptr(), slots.data_ptr(), tokens,
+              base.data_ptr() if base is not None else None, out.data_ptr(), u.data_ptr() if u is not None else None,
+              ws.data_ptr(), ws.numel())
+        return out if u is None else (out, u)
+
+    def backward(self, grad_y: torch.Tensor, x: torch.Tensor, u: torch.Tensor, slots: torch.Tensor,
+                 grad_x_base: Optional[torch.Tensor] = None, grad_x: Optional[torch.Tensor] = None,
+                 grad_a: Optional[torch.Tensor] = None, grad_b: Optional[torch.Tensor] = None, need_x: bool = True,
+                 stream=None):
+        """(grad_a, grad_b, grad_x), bf16, shaped as a, b and x; grad_x is
+        None with need_x False.  grad_x_base: the gradient through the
+        projection (None: zeros); grad_x may be grad_x_base."""
+        tokens = self._tokens(x, slots)
+        _require(grad_y, "grad_y", (tokens, self.rows), (torch.bfloat16,), self.device)
+        _require(u, "u", (tokens, self.rank), (torch.float32,), self.device)
+        if not need_x and (grad_x is not None or grad_x_base is not None):
+            raise E8qError("grad_x given with need_x False")
+        if grad_x_base is not None:
+            _require(grad_x_base, "grad_x_base", (tokens, self.cols), (torch.bfloat16,), self.device)
+        outs = []
+        ad = self._c()
+        with _allocating_on(stream):
+            for name, t, shape in (("grad_a", grad_a, self.a.shape), ("grad_b", grad_b, self.b.shape),
+                                   ("grad_x", grad_x, (tokens, self.cols))):
+                if t is not None:
+                    _require(t, name, shape, (torch.bfloat16,), self.device)
+                elif name != "grad_x" or need_x:
+                    t = self._out(name, shape, torch.bfloat16)
+                outs.append(t)
+            ws = self._ws(ad, tokens, 1)
+        ga, gb, gx = outs
+        _call("e8q_lora_backward", self.device, stream, ctypes.byref(ad), grad_y.data_ptr(), x.data_ptr(), u.data_ptr(),
+              slots.data_ptr(), tokens, ga.data_ptr(), gb.data_ptr(),
+              grad_x_base.data_ptr() if grad_x_base is not None else None, gx.data_ptr() if gx is not None else None,
+              ws.data_ptr(), ws.numel())
+        return ga, gb, gx

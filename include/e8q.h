@@ -410,6 +410,76 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
                              int32_t latent_dtype, int64_t rows, int64_t cols, void* ws, size_t ws_bytes,
                              e8q_stream stream);
 
+/* Low-rank adapters beside one projection of `rows` outputs and `cols`
+ * inputs (the weights as e8q_dequant_gemv multiplies them): adapter i adds
+ * scale[i] B_i A_i to the projection's matrix.  Lower ranks than `rank` are
+ * padded with zero rows of A and columns of B. */
+typedef struct e8q_adapters {
+    const void* a;       /* [n][rank][cols] bf16, 16-byte aligned */
+    const void* b;       /* [n][rows][rank] bf16, 16-byte aligned */
+    const float* scale;  /* [n] */
+    int64_t rows;        /* multiple of 8, up to 2^20 */
+    int64_t cols;        /* multiple of 8, up to 2^20 */
+    int32_t n;           /* 0 .. 2048 */
+    int32_t rank;        /* multiple of 8, 8 .. 128 */
+} e8q_adapters;
+
+/*
+ * Workspace bytes e8q_lora (backward = 0) or e8q_lora_backward (otherwise)
+ * needs for this many tokens (exact; the same on every device; 256 for
+ * arguments the call would reject).  Needs no GPU.
+ */
+size_t e8q_lora_workspace_bytes(const e8q_adapters* ad /* host */, int64_t tokens, int32_t backward);
+
+/*
+ * Adapters of many requests at once, added to a shared projection's output:
+ *   u[t] = A_a x[t],  y[t] = base[t] + scale[a] B_a u[t],  a = slots[t].
+ * A token whose slot lies outside 0 .. n-1 has no adapter: y[t] = base[t],
+ * u[t] = 0.  Slots may come in any order and repeat; the result does not
+ * depend on how tokens of one adapter are placed.
+ *
+ * x: [tokens][cols] bf16; slots: [tokens] int32; base: [tokens][rows] bf16
+ * (e8q_dequant_gemv's or e8q_dequant_gemm's y), or NULL for zeros; y:
+ * [tokens][rows] bf16, may be base itself; u: [tokens][rank] fp32 for the
+ * backward pass, or NULL.  All but slots 16-byte aligned; 0 <= tokens <=
+ * 65536.  No other two of y, u and the inputs may overlap.  ws: device memory of
+ * at least e8q_lora_workspace_bytes(ad, tokens, 0) bytes, 256-byte aligned,
+ * owned by the caller, overwritten; two calls that may run at the same time
+ * need one each.
+ *
+ * Arithmetic: fp32 sums of exact products; scale[a] u enters the second
+ * product as a bf16 high plus a bf16 low part (about 16 bits); y is rounded
+ * once.  The order of the sums follows from the shapes and the slots alone,
+ * so repeated calls give the same bits on any device.
+ * Asynchronous on `stream`; errors: INVALID_ARG, UNSUPPORTED (limits above),
+ * WORKSPACE, CUDA.
+ */
+e8q_status e8q_lora(const e8q_adapters* ad /* host */, const void* x_bf16, const int32_t* slots, int64_t tokens,
+                    const void* base_bf16, void* y_bf16, float* u, void* ws, size_t ws_bytes, e8q_stream stream);
+
+/*
+ * Backward of e8q_lora, given the gradient of y and the forward's u:
+ *   v[t] = scale[a] B_a^T grad_y[t],
+ *   grad_a[i] = sum over t with slots[t] = i of v[t] x[t]^T          [n][rank][cols],
+ *   grad_b[i] = scale[i] sum over the same t of grad_y[t] u[t]^T    [n][rows][rank],
+ *   grad_x[t] = grad_x_base[t] + A_a^T v[t]                         [tokens][cols].
+ * grad_a and grad_b (bf16) are written whole, zeros for adapters without a
+ * token.  grad_x_base (bf16): the gradient through the projection itself, or
+ * NULL for zeros; grad_x (bf16): may be grad_x_base itself, or NULL (with
+ * grad_x_base NULL) where it is not needed.  Tokens without an adapter add
+ * nothing; their grad_x is grad_x_base.  Alignment and limits as for
+ * e8q_lora; outputs may overlap no input and no other output.  ws as there,
+ * of e8q_lora_workspace_bytes(ad, tokens, 1) bytes.
+ *
+ * Arithmetic: fp32 sums; scale u and v as bf16 high + low parts; every
+ * output rounded once.  Same bits on repeated calls, on any device.
+ * Asynchronous on `stream`; errors as for e8q_lora.
+ */
+e8q_status e8q_lora_backward(const e8q_adapters* ad /* host */, const void* grad_y_bf16, const void* x_bf16,
+                             const float* u, const int32_t* slots, int64_t tokens, void* grad_a_bf16,
+                             void* grad_b_bf16, const void* grad_x_base_bf16, void* grad_x_bf16, void* ws,
+                             size_t ws_bytes, e8q_stream stream);
+
 /*
  * Project + encode without allocating anything: the same computation and
  * outputs as e8q_project_encode, for callers that cannot allocate device
