@@ -23,8 +23,10 @@ inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 // Launch with programmatic stream serialisation: the kernel may start while
 // the previous kernel on the stream is finishing; it waits for that
 // kernel's results with griddepcontrol.wait.
+// The first kernel of a call is launched without it (`overlaps` false).
 template <typename P>
-e8q_status launch_pdl(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& params) {
+e8q_status launch_pdl(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& params,
+                      bool overlaps = true) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -34,7 +36,7 @@ e8q_status launch_pdl(void (*kernel)(P), dim3 grid, int threads, size_t smem, cu
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = overlaps ? 1 : 0;
     return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, params));
 }
 template <typename P>

@@ -34,11 +34,12 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
     return g;
 }
 
-// columns a CTA of k_lr_down: at most 4,096 (a warp's sum then has at most
-// 64 MMAs of 16 columns), fewer where there are few tiles
+// Columns a CTA of k_lr_down: as many as let all CTAs run at once, two an SM
+// (a second wave would wait for the first), at most 4,096 so that a warp's sum
+// has at most 64 MMAs.
 int64_t down_columns(const LrGeom& g, int64_t cols) {
     const int64_t least = ceil_div(cols, 4096), most = ceil_div(cols, 256);
-    const int64_t splits = std::min(most, std::max(least, ceil_div(kFill, g.tiles * g.zparts)));
+    const int64_t splits = std::min(most, std::max(least, 2 * 148 / (g.tiles * g.zparts)));
     return ceil_div(ceil_div(cols, splits), 256) * 256;
 }
 
@@ -83,23 +84,33 @@ e8q_status check(const e8q_adapters* a, int64_t tokens) {
 
 size_t plan_smem(int n) { return static_cast<size_t>(n + 2) * 16 + static_cast<size_t>(n + 1) * 64; }
 
-template <bool kSmall, bool kTrans>
-e8q_status down_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(k_lr_down<1, kSmall, kTrans>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(lr_down_smem(1, kSmall, kTrans)));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_lr_down<2, kSmall, kTrans>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(lr_down_smem(2, kSmall, kTrans)));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_lr_down<4, kSmall, kTrans>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(lr_down_smem(4, kSmall, kTrans)));
-    return cuda_ok(e);
+template <typename K>
+e8q_status allow(K kernel, size_t smem) {
+    return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
 }
 
-template <int NT>
-e8q_status grad_attributes() {
-    return cuda_ok(cudaFuncSetAttribute(k_lr_grad<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(lr_grad_smem(NT))));
+template <int MT, bool kTrans>
+e8q_status allow_down() {
+    e8q_status st = allow(k_lr_down<MT, kTrans>, lr_down_smem(MT, kTrans));
+    return st == E8Q_OK ? allow(k_lr_down_few<MT, kTrans>, lr_down_few_smem(MT, kTrans)) : st;
+}
+
+template <int KS, bool kTrans>
+e8q_status allow_up() {
+    e8q_status st = allow(k_lr_up<KS, false, kTrans>, lr_up_smem(KS, false, kTrans));
+    return st == E8Q_OK ? allow(k_lr_up<KS, true, kTrans>, lr_up_smem(KS, true, kTrans)) : st;
+}
+
+template <bool kTrans>
+e8q_status allow_all() {
+    e8q_status st = allow_down<1, kTrans>();
+    if (st == E8Q_OK) st = allow_down<2, kTrans>();
+    if (st == E8Q_OK) st = allow_down<4, kTrans>();
+    if (st == E8Q_OK) st = allow_up<1, kTrans>();
+    if (st == E8Q_OK) st = allow_up<2, kTrans>();
+    if (st == E8Q_OK) st = allow_up<4, kTrans>();
+    if (st == E8Q_OK) st = allow_up<8, kTrans>();
+    return st;
 }
 
 // Shared-memory limits of the kernels, once per device.
@@ -111,16 +122,13 @@ e8q_status ensure_lora() {
     if (dev < 0 || dev >= 64) return E8Q_ERR_UNSUPPORTED;
     std::lock_guard<std::mutex> lock(mu);
     if (ready[dev]) return E8Q_OK;
-    e8q_status st = cuda_ok(cudaFuncSetAttribute(k_lr_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(plan_smem(kLrMaxAdapters))));
-    if (st == E8Q_OK) st = down_attributes<false, false>();
-    if (st == E8Q_OK) st = down_attributes<false, true>();
-    if (st == E8Q_OK) st = down_attributes<true, false>();
-    if (st == E8Q_OK) st = down_attributes<true, true>();
-    if (st == E8Q_OK) st = grad_attributes<2>();
-    if (st == E8Q_OK) st = grad_attributes<4>();
-    if (st == E8Q_OK) st = grad_attributes<8>();
-    if (st == E8Q_OK) st = grad_attributes<16>();
+    e8q_status st = allow(k_lr_plan, plan_smem(kLrMaxAdapters));
+    if (st == E8Q_OK) st = allow_all<false>();
+    if (st == E8Q_OK) st = allow_all<true>();
+    if (st == E8Q_OK) st = allow(k_lr_grad<2>, lr_grad_smem(2));
+    if (st == E8Q_OK) st = allow(k_lr_grad<4>, lr_grad_smem(4));
+    if (st == E8Q_OK) st = allow(k_lr_grad<8>, lr_grad_smem(8));
+    if (st == E8Q_OK) st = allow(k_lr_grad<16>, lr_grad_smem(16));
     ready[dev] = st == E8Q_OK;
     return st;
 }
@@ -143,9 +151,11 @@ e8q_status launch_plan(const e8q_adapters& a, const int32_t* slots, int64_t toke
 }
 
 template <bool kTrans>
-e8q_status launch_down(const e8q_adapters& a, const void* z, const void* weights, int64_t cols, int64_t tokens,
-                       const LrGeom& g, const LrWs& l, unsigned char* w, cudaStream_t s) {
+e8q_status launch_down(const e8q_adapters& a, const int32_t* slots, const void* z, const void* weights, int64_t cols,
+                       int64_t tokens, const LrGeom& g, const LrWs& l, unsigned char* w, cudaStream_t s, bool overlaps) {
     LrDownParams p;
+    p.slots = slots;
+    p.n = a.n;
     p.head = reinterpret_cast<const int32_t*>(w + l.head);
     p.order = reinterpret_cast<const int32_t*>(w + l.order);
     p.tiles = reinterpret_cast<const LrTile*>(w + l.tiles);
@@ -157,22 +167,30 @@ e8q_status launch_down(const e8q_adapters& a, const void* z, const void* weights
     p.rank = a.rank;
     p.per = static_cast<int32_t>(down_columns(g, cols));
     const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.per)), static_cast<unsigned>(g.zparts));
-    const bool small = g.tile == kLrSmallTile;
-    const size_t smem = lr_down_smem(g.mt, small, kTrans);
-    if (small) {
-        if (g.mt == 1) return launch_pdl(k_lr_down<1, true, kTrans>, grid, kLrDownThreads, smem, s, p);
-        if (g.mt == 2) return launch_pdl(k_lr_down<2, true, kTrans>, grid, kLrDownThreads, smem, s, p);
-        return launch_pdl(k_lr_down<4, true, kTrans>, grid, kLrDownThreads, smem, s, p);
+    if (g.tile == kLrSmallTile) {
+        const size_t smem = lr_down_few_smem(g.mt, kTrans);
+        if (g.mt == 1) return launch_pdl(k_lr_down_few<1, kTrans>, grid, kLrDownThreads, smem, s, p, overlaps);
+        if (g.mt == 2) return launch_pdl(k_lr_down_few<2, kTrans>, grid, kLrDownThreads, smem, s, p, overlaps);
+        return launch_pdl(k_lr_down_few<4, kTrans>, grid, kLrDownThreads, smem, s, p, overlaps);
     }
-    if (g.mt == 1) return launch_pdl(k_lr_down<1, false, kTrans>, grid, kLrDownThreads, smem, s, p);
-    if (g.mt == 2) return launch_pdl(k_lr_down<2, false, kTrans>, grid, kLrDownThreads, smem, s, p);
-    return launch_pdl(k_lr_down<4, false, kTrans>, grid, kLrDownThreads, smem, s, p);
+    const size_t smem = lr_down_smem(g.mt, kTrans);
+    if (g.mt == 1) return launch_pdl(k_lr_down<1, kTrans>, grid, kLrDownThreads, smem, s, p);
+    if (g.mt == 2) return launch_pdl(k_lr_down<2, kTrans>, grid, kLrDownThreads, smem, s, p);
+    return launch_pdl(k_lr_down<4, kTrans>, grid, kLrDownThreads, smem, s, p);
+}
+
+template <int KS, bool kTrans>
+e8q_status launch_up_rank(bool small, dim3 grid, cudaStream_t s, const LrUpParams& p) {
+    return small ? launch_pdl(k_lr_up<KS, true, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, true, kTrans), s, p)
+                 : launch_pdl(k_lr_up<KS, false, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, false, kTrans), s, p);
 }
 
 template <bool kTrans>
-e8q_status launch_up(const e8q_adapters& a, const void* weights, const void* base, void* out, float* sum, int64_t cols,
+e8q_status launch_up(const e8q_adapters& a, const int32_t* slots, const void* weights, const void* base, void* out, float* sum, int64_t cols,
                      int64_t sum_cols, int64_t tokens, const LrGeom& g, const LrWs& l, unsigned char* w, cudaStream_t s) {
     LrUpParams p;
+    p.slots = slots;
+    p.n = a.n;
     p.head = reinterpret_cast<const int32_t*>(w + l.head);
     p.order = reinterpret_cast<const int32_t*>(w + l.order);
     p.tiles = reinterpret_cast<const LrTile*>(w + l.tiles);
@@ -187,9 +205,14 @@ e8q_status launch_up(const e8q_adapters& a, const void* weights, const void* bas
     p.rank = a.rank;
     p.splits = static_cast<int32_t>(ceil_div(sum_cols, down_columns(g, sum_cols)));
     // long ranges share the factors' preparation, short ones fill the GPU
-    p.range = g.tiles * ceil_div(cols, 512) >= kFill ? 512 : 128;
+    p.range = static_cast<int32_t>(kLrUpCols);
+    while (p.range < 1024 && g.tiles * ceil_div(cols, 2 * p.range) >= kFill) p.range *= 2;
     const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.range)));
-    return launch_pdl(k_lr_up<kTrans>, grid, kLrUpThreads, lr_up_smem(a.rank), s, p);
+    const bool small = g.tile == kLrSmallTile;
+    if (a.rank <= 16) return launch_up_rank<1, kTrans>(small, grid, s, p);
+    if (a.rank <= 32) return launch_up_rank<2, kTrans>(small, grid, s, p);
+    if (a.rank <= 64) return launch_up_rank<4, kTrans>(small, grid, s, p);
+    return launch_up_rank<8, kTrans>(small, grid, s, p);
 }
 
 }  // namespace
@@ -223,9 +246,9 @@ e8q_status e8q_lora(const e8q_adapters* a, const void* x, const int32_t* slots, 
     if (st != E8Q_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     unsigned char* w = static_cast<unsigned char*>(ws);
-    st = launch_plan(*a, slots, tokens, g, l, w, s);
-    if (st == E8Q_OK) st = launch_down<false>(*a, x, a->a, a->cols, tokens, g, l, w, s);
-    if (st == E8Q_OK) st = launch_up<false>(*a, a->b, base, y, u, a->rows, a->cols, tokens, g, l, w, s);
+    if (g.tile != kLrSmallTile) st = launch_plan(*a, slots, tokens, g, l, w, s);
+    if (st == E8Q_OK) st = launch_down<false>(*a, slots, x, a->a, a->cols, tokens, g, l, w, s, g.tile != kLrSmallTile);
+    if (st == E8Q_OK) st = launch_up<false>(*a, slots, a->b, base, y, u, a->rows, a->cols, tokens, g, l, w, s);
     return st;
 }
 
@@ -266,7 +289,7 @@ e8q_status e8q_lora_backward(const e8q_adapters* a, const void* grad_y, const vo
     if (st != E8Q_OK) return st;
     unsigned char* w = static_cast<unsigned char*>(ws);
     st = launch_plan(*a, slots, tokens, g, l, w, s);
-    if (st == E8Q_OK) st = launch_down<true>(*a, grad_y, a->b, a->rows, tokens, g, l, w, s);
+    if (st == E8Q_OK) st = launch_down<true>(*a, slots, grad_y, a->b, a->rows, tokens, g, l, w, s, true);
     if (st == E8Q_OK && a->n > 0) {
         LrSplitParams sp;
         sp.head = reinterpret_cast<const int32_t*>(w + l.head);
@@ -308,7 +331,7 @@ e8q_status e8q_lora_backward(const e8q_adapters* a, const void* grad_y, const vo
         if (st == E8Q_OK) st = launch_pdl(k_lr_join, jgrid, 256, 0, s, gp);
     }
     if (st == E8Q_OK && grad_x)
-        st = launch_up<true>(*a, a->a, grad_x_base, grad_x, nullptr, a->cols, a->rows, tokens, g, l, w, s);
+        st = launch_up<true>(*a, slots, a->a, grad_x_base, grad_x, nullptr, a->cols, a->rows, tokens, g, l, w, s);
     return st;
 }
 

@@ -5,23 +5,17 @@
 //   v_t = s_a B_a^T gy_t,   gx_t = gx0_t + A_a^T v_t
 //   gA_a = sum_t v_t x_t^T,   gB_a = sum_t gy_t (s_a u_t)^T
 //
-// The tokens are grouped by adapter first (k_lr_plan); everything after it
-// works on tiles of up to 64 (8 in small batches) tokens of one adapter:
+// The tokens are grouped by adapter first (k_lr_plan; in small batches each
+// CTA groups for itself); everything after it works on tiles of up to 64 (8
+// in small batches) tokens of one adapter:
 //
 //   k_lr_down   p = W z, a long sum over the columns of z and a short result
 //               (u from x and A; v / s from gy and B): tensor cores with the
-//               rank as M and the tokens as N (8 a tile, so that one token wastes
-//               7 columns, not 15), operands straight from global memory in
-//               16-byte loads.  The sum's order is free, so lane q takes the
-//               columns 8q..8q+7 of a 32-column block as they lie in memory and
-//               both operands use that order.  The columns are split over the
-//               warps of a CTA and over CTAs; partial sums are added in a
-//               fixed order;
+//               rank as M and the tokens as N.  The columns are split over the
+//               warps of a CTA and over CTAs; partial sums are added in a fixed
+//               order;
 //   k_lr_up     out = base + W w, a short sum and a long result (y from u and
-//               B; gx from v and A): tokens as M, columns as N; the columns of
-//               the four 8-column MMA tiles of a 32-column chunk are dealt so
-//               that a lane ends up with 8 neighbouring ones (16-byte loads of
-//               base and stores of out);
+//               B; gx from v and A): tokens as M, columns as N;
 //   k_lr_split  (backward) w = s u and v as bf16 high + low parts;
 //   k_lr_grad   sums over tokens: gB from gy and s u, gA from x and v, both in
 //               one launch.  z^T and w come from shared memory by transposing
@@ -87,15 +81,28 @@ __global__ void __launch_bounds__(kLrPlanThreads) k_lr_plan(const __grid_constan
     const int per = ((p.tokens + 1023) / 1024) * 32, t0 = warp * per, t1 = min(p.tokens, t0 + per);
     uint16_t* mine = hist + warp * nb;
     const unsigned below = (1u << lane) - 1u;
-    for (int t = t0; t < t1; t += 32) {
-        int bin = nb;  // past the end: matched only by its like
-        if (t + lane < t1) {
-            const int s = __ldg(p.slots + t + lane);
-            bin = (s >= 0 && s < p.n) ? s : p.n;
+    auto bins = [&](int t, int (&bin)[8]) {  // of 256 tokens; past the range: nb, matched only by its like
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = t + 32 * i + lane;
+            bin[i] = at < t1 ? __ldg(p.slots + at) : 0;
         }
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, bin);
-        if (bin < nb && (peers & below) == 0) mine[bin] = static_cast<uint16_t>(mine[bin] + __popc(peers));
-        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = t + 32 * i + lane;
+            bin[i] = at >= t1 ? nb : (bin[i] >= 0 && bin[i] < p.n) ? bin[i] : p.n;
+        }
+    };
+    for (int t = t0; t < t1; t += 256) {
+        int bin[8];
+        bins(t, bin);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (t + 32 * i >= t1) break;
+            const unsigned peers = __match_any_sync(0xFFFFFFFFu, bin[i]);
+            if (bin[i] < nb && (peers & below) == 0) mine[bin[i]] = static_cast<uint16_t>(mine[bin[i]] + __popc(peers));
+            __syncwarp();
+        }
     }
     __syncthreads();
     // bins 3 tid .. 3 tid + 2: counts before each warp, then the scan over the bins
@@ -155,20 +162,21 @@ __global__ void __launch_bounds__(kLrPlanThreads) k_lr_plan(const __grid_constan
         }
     }
     __syncthreads();
-    for (int t = t0; t < t1; t += 32) {
-        int bin = nb;
-        if (t + lane < t1) {
-            const int s = __ldg(p.slots + t + lane);
-            bin = (s >= 0 && s < p.n) ? s : p.n;
+    for (int t = t0; t < t1; t += 256) {
+        int bin[8];
+        bins(t, bin);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (t + 32 * i >= t1) break;
+            const unsigned peers = __match_any_sync(0xFFFFFFFFu, bin[i]);
+            const int before = bin[i] < nb ? mine[bin[i]] : 0;
+            __syncwarp();
+            if (bin[i] < nb) {
+                p.order[s_tok[bin[i]] + before + __popc(peers & below)] = t + 32 * i + lane;
+                if ((peers & below) == 0) mine[bin[i]] = static_cast<uint16_t>(before + __popc(peers));
+            }
+            __syncwarp();
         }
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, bin);
-        const int before = bin < nb ? mine[bin] : 0;
-        __syncwarp();
-        if (bin < nb) {
-            p.order[s_tok[bin] + before + __popc(peers & below)] = t + lane;
-            if ((peers & below) == 0) mine[bin] = static_cast<uint16_t>(before + __popc(peers));
-        }
-        __syncwarp();
     }
     const int ntiles = s_tile[nb], nunits = s_unit[p.n];
     for (int k = tid; k < ntiles; k += kLrPlanThreads) {
@@ -218,6 +226,12 @@ __device__ __forceinline__ void ldsm_t4(unsigned (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
+__device__ __forceinline__ void ldsm_4(unsigned (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 // 16-byte copy, or 16 zero bytes where it is off (nothing is read then)
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -239,15 +253,66 @@ __device__ __forceinline__ void lr_split2(float a, float b, unsigned& high, unsi
     low = lr_pack(fabsf(ra) <= fabsf(a) ? ra : 0.f, fabsf(rb) <= fabsf(b) ? rb : 0.f);
 }
 
+// Small batches (up to kLrSmallTokens tokens): every CTA finds its own tile of
+// up to 8 tokens, which costs less than a launch that would tell it.  A tile
+// begins at each token that has a multiple of 8 tokens of its adapter before
+// it; tiles are numbered by their first token.
+struct LrSmall {
+    int slot[kLrSmallTokens];  // n: no adapter
+    int before[kLrSmallTokens];
+    int warp_heads[kLrSmallTokens / 32];
+    int head;
+    int tok[kLrSmallTile];
+};
+
+__device__ __forceinline__ LrTile lr_find_tile(LrSmall& s, const int32_t* slots, int tokens, int n, int index) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int mine = -1, before = 0;
+    if (tid < kLrSmallTokens) {
+        if (tid < tokens) {
+            mine = __ldg(slots + tid);
+            if (mine < 0 || mine >= n) mine = n;
+        }
+        s.slot[tid] = mine;
+    }
+    if (tid == 0) s.head = -1;
+    __syncthreads();
+    bool head = false;
+    if (tid < kLrSmallTokens) {
+        for (int j = 0; j < min(tokens, 32 * warp); ++j) before += s.slot[j] == mine;
+        before += __popc(__match_any_sync(0xFFFFFFFFu, mine) & ((1u << lane) - 1u));
+        s.before[tid] = before;
+        head = tid < tokens && (before & (kLrSmallTile - 1)) == 0;
+        const unsigned heads = __ballot_sync(0xFFFFFFFFu, head);
+        if (lane == 0) s.warp_heads[warp] = __popc(heads);
+        before = __popc(heads & ((1u << lane) - 1u));  // heads before this token in its warp
+    }
+    __syncthreads();
+    if (head) {
+        for (int w = 0; w < warp; ++w) before += s.warp_heads[w];
+        if (before == index) s.head = tid;
+    }
+    __syncthreads();
+    LrTile t{0, 0, -2, 0};
+    if (s.head < 0) return t;  // no such tile
+    const int h = s.head, first = s.before[h], slot = s.slot[h];
+    if (tid < kLrSmallTokens && mine == slot && s.before[tid] >= first && s.before[tid] < first + kLrSmallTile)
+        s.tok[s.before[tid] - first] = tid;
+    t.len = __syncthreads_count(tid < kLrSmallTokens && mine == slot && s.before[tid] >= first && s.before[tid] < first + kLrSmallTile);
+    t.slot = slot == n ? -1 : slot;
+    return t;
+}
+
 // ------------------------------------------------------------------ p = W z
 struct LrDownParams {
     const int32_t* head;
     const int32_t* order;
     const LrTile* tiles;
+    const int32_t* slots;
     const uint16_t* z;  // [tokens][cols]
     const uint16_t* w;  // [n][rank][cols], or [n][cols][rank] (kTrans)
     float* part;        // [split][tokens][rank]
-    int32_t tokens, cols, rank;
+    int32_t tokens, cols, rank, n;
     int32_t per;        // columns a CTA, a multiple of 256
 };
 
@@ -255,60 +320,35 @@ struct LrDownParams {
 // eight rows of each 8x8 matrix of the MMA's A operand follow one another.
 __device__ __forceinline__ int lr_stage_row(int n) { return 16 * ((n >> 2) & 1) + 8 * ((n >> 1) & 1) + 2 * (n >> 3) + (n & 1); }
 
-// MT: 16-row tiles of the rank (4 at most: higher ranks in gridDim.z parts).
-// kSmall: tiles of 8 tokens, 8 warps along the columns; else 64 tokens, 2 x 4.
-template <int MT, bool kSmall, bool kTrans>
-__global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constant__ LrDownParams p) {
-    constexpr int KW = kSmall ? 8 : 4, NT = kSmall ? 1 : 4;
-    constexpr int STEP = 32 * KW;                // columns a round
-    constexpr int ROW = MT * 16 * 2 + 16;        // bytes of a staged row (kTrans), padded against bank conflicts
+// Tiles of up to 8 tokens: 8 warps along the columns, z and the weights
+// straight from global memory in 16-byte loads.  MT: 16-row tiles of the
+// rank (4 at most: higher ranks in gridDim.z parts).
+template <int MT, bool kTrans>
+__global__ void __launch_bounds__(kLrDownThreads) k_lr_down_few(const __grid_constant__ LrDownParams p) {
+    constexpr int KW = 8, STEP = 32 * KW;   // columns a round
+    constexpr int ROW = MT * 16 * 2 + 16;   // bytes of a staged row (kTrans), padded against bank conflicts
     extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ LrSmall s_small;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
-    const int kq = kSmall ? warp : (warp & 3), th = kSmall ? 0 : (warp >> 2);
     pdl_wait();
     pdl_launch_dependents();
-    if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
-    const LrTile tile = p.tiles[blockIdx.x];
+    const LrTile tile = lr_find_tile(s_small, p.slots, p.tokens, p.n, blockIdx.x);
     if (tile.slot < 0) return;
     const int k0 = static_cast<int>(blockIdx.y) * p.per, k1 = min(p.cols, k0 + p.per);
     const int r0 = static_cast<int>(blockIdx.z) * 64;
     const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
-    const uint16_t* zr[NT];
-    bool on[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int t = 32 * th + 8 * i + c;
-        on[i] = t < tile.len;
-        zr[i] = p.z + static_cast<size_t>(on[i] ? p.order[tile.first + t] : 0) * p.cols;
-    }
-    const int live = min(NT, (tile.len - 32 * th + 7) >> 3);  // token tiles with a token (the same in the whole warp)
-    float acc[MT][NT][4];
+    const bool on = c < tile.len;
+    const uint16_t* zr = p.z + static_cast<size_t>(on ? s_small.tok[c] : 0) * p.cols;
+    float acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[m][e] = 0.f;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-
-    auto load_z = [&](int kb, uint4 (&x)[NT]) {
+    auto load_z = [&](int kb) {
         const int k = kb + 8 * q;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            x[i] = (on[i] && k < k1) ? __ldg(reinterpret_cast<const uint4*>(zr[i] + k)) : zero;
+        return (on && k < k1) ? __ldg(reinterpret_cast<const uint4*>(zr + k)) : zero;
     };
-    auto multiply = [&](const unsigned (&a)[MT][2][4], const uint4 (&x)[NT]) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if (i >= live) break;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                lr_mma(acc[m][i], a[m][0][0], a[m][0][1], a[m][0][2], a[m][0][3], x[i].x, x[i].y);
-                lr_mma(acc[m][i], a[m][1][0], a[m][1][1], a[m][1][2], a[m][1][3], x[i].z, x[i].w);
-            }
-        }
-    };
-
     if (!kTrans) {
         auto load_w = [&](int kb, uint4 (&v)[MT][2]) {
             const int k = kb + 8 * q;
@@ -320,23 +360,20 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constan
                     v[m][h] = (r < p.rank && k < k1) ? __ldg(reinterpret_cast<const uint4*>(w + static_cast<size_t>(r) * p.cols + k)) : zero;
                 }
         };
-        uint4 x[NT], v[MT][2];
-        int kb = k0 + 32 * kq;
-        load_z(kb, x);
+        uint4 x, v[MT][2];
+        int kb = k0 + 32 * warp;
+        x = load_z(kb);
         load_w(kb, v);
         for (; kb < k1; kb += STEP) {
-            uint4 xn[NT], vn[MT][2];
-            load_z(kb + STEP, xn);
+            uint4 vn[MT][2];
+            const uint4 xn = load_z(kb + STEP);
             load_w(kb + STEP, vn);
-            unsigned a[MT][2][4];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                a[m][0][0] = v[m][0].x; a[m][0][1] = v[m][1].x; a[m][0][2] = v[m][0].y; a[m][0][3] = v[m][1].y;
-                a[m][1][0] = v[m][0].z; a[m][1][1] = v[m][1].z; a[m][1][2] = v[m][0].w; a[m][1][3] = v[m][1].w;
+                lr_mma(acc[m], v[m][0].x, v[m][1].x, v[m][0].y, v[m][1].y, x.x, x.y);
+                lr_mma(acc[m], v[m][0].z, v[m][1].z, v[m][0].w, v[m][1].w, x.z, x.w);
             }
-            multiply(a, x);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) x[i] = xn[i];
+            x = xn;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 v[m][0] = vn[m][0];
@@ -356,35 +393,186 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constan
             }
             cp_async_commit();
         };
-        uint4 x[NT];
         stage(k0, 0);
-        load_z(k0 + 32 * kq, x);
+        uint4 x = load_z(k0 + 32 * warp);
         int buf = 0;
         for (int kr = k0; kr < k1; kr += STEP, buf ^= 1) {
-            uint4 xn[NT];
-            load_z(kr + STEP + 32 * kq, xn);
+            const uint4 xn = load_z(kr + STEP + 32 * warp);
             cp_async_wait<0>();
             __syncthreads();  // the round's weights are there, and the other buffer is read
             if (kr + STEP < k1) stage(kr + STEP, buf ^ 1);
-            unsigned a[MT][2][4];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    ldsm_t4(a[m][h], base + (buf * STEP + 32 * kq + 16 * h + 8 * (lane >> 4) + (lane & 7)) * ROW +
-                                         32 * m + 16 * ((lane >> 3) & 1));
-            multiply(a, x);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) x[i] = xn[i];
+                for (int h = 0; h < 2; ++h) {
+                    unsigned a[4];
+                    ldsm_t4(a, base + (buf * STEP + 32 * warp + 16 * h + 8 * (lane >> 4) + (lane & 7)) * ROW + 32 * m +
+                                   16 * ((lane >> 3) & 1));
+                    lr_mma(acc[m], a[0], a[1], a[2], a[3], h ? x.z : x.x, h ? x.w : x.y);
+                }
+            x = xn;
         }
         __syncthreads();  // the staging memory becomes the reduction's
     }
+
+    // the warps' sums, in order
+    float* red = reinterpret_cast<float*>(smem);
+    constexpr int V = MT * 4;
+    if (warp > 0)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[((warp - 1) * V + 4 * m + e) * 32 + lane] = acc[m][e];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int k = 0; k < KW - 1; ++k)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][e] += red[(k * V + 4 * m + e) * 32 + lane];
+    float* out = p.part + static_cast<size_t>(blockIdx.y) * p.tokens * p.rank;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int t = 2 * q + e;
+        if (t >= tile.len) continue;
+        float* row = out + static_cast<size_t>(s_small.tok[t]) * p.rank;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = r0 + 16 * m + 8 * h + c;
+                if (r < p.rank) row[r] = acc[m][2 * h + e];
+            }
+    }
+}
+
+__host__ __device__ constexpr size_t lr_down_few_smem(int mt, bool trans) {
+    const size_t red = size_t{7} * mt * 4 * 32 * 4;
+    const size_t stage = trans ? size_t{2} * 256 * (static_cast<size_t>(mt) * 32 + 16) : 0;
+    return red > stage ? red : stage;
+}
+
+// Tiles of up to 64 tokens: z [64][128 columns] and the weights of the same
+// columns come through shared memory, three or four rounds deep (two CTAs an
+// SM: a round's compute is short, and the loads of the next ones have to be out).  8 warps: 4 along the
+// round's columns, 2 along the tokens.
+constexpr int kLrRound = 128;
+__host__ __device__ constexpr int lr_down_stages(int mt) { return mt == 4 ? 3 : 4; }
+
+template <int MT, bool kTrans>
+__global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constant__ LrDownParams p) {
+    constexpr int NT = 4, kStages = lr_down_stages(MT);
+    constexpr int ZB = kLrTile * kLrRound * 2;                           // 16-byte pieces xored with the row
+    constexpr int ROW = MT * 16 * 2 + 16;                                // staged row (kTrans), padded
+    constexpr int WB = kTrans ? kLrRound * ROW : MT * 16 * kLrRound * 2;  // (else) pieces xored with the row
+    constexpr int STAGE = ZB + WB;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int s_tok[kLrTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
+    const int kq = warp & 3, th = warp >> 2;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
+    const LrTile tile = p.tiles[blockIdx.x];
+    if (tile.slot < 0) return;
+    const int k0 = static_cast<int>(blockIdx.y) * p.per, k1 = min(p.cols, k0 + p.per);
+    const int r0 = static_cast<int>(blockIdx.z) * 64;
+    const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
+    if (tid < tile.len) s_tok[tid] = p.order[tile.first + tid];
+    __syncthreads();
+    const uint32_t base = smem_addr(smem);
+    // this thread's pieces of a round of z: rows tid / 16 + 16 i, piece tid % 16
+    const uint16_t* zr[4];
+    bool on[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (tid >> 4) + 16 * i;
+        on[i] = row < tile.len;
+        zr[i] = p.z + static_cast<size_t>(on[i] ? s_tok[row] : 0) * p.cols + 8 * (tid & 15);
+    }
+    auto stage = [&](int kb, int buf) {
+        const uint32_t d = base + buf * STAGE;
+        if (kb < k1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (tid >> 4) + 16 * i;
+                const bool in = on[i] && kb + 8 * (tid & 15) < k1;
+                cp_async16_or_zero(d + row * (kLrRound * 2) + 16 * ((tid & 15) ^ (row & 7)), in ? zr[i] + kb : p.z, in);
+            }
+            if (kTrans) {
+                constexpr int CH = 2 * MT;
+#pragma unroll
+                for (int i = tid; i < kLrRound * CH; i += kLrDownThreads) {
+                    const int n = i / CH, piece = i - n * CH, k = kb + n, r = r0 + 8 * piece;
+                    const bool in = k < k1 && r < p.rank;
+                    cp_async16_or_zero(d + ZB + n * ROW + 16 * piece, in ? w + static_cast<size_t>(k) * p.rank + r : w, in);
+                }
+            } else {
+#pragma unroll
+                for (int i = tid; i < MT * 16 * 16; i += kLrDownThreads) {
+                    const int row = i >> 4, piece = i & 15, k = kb + 8 * piece;
+                    const bool in = r0 + row < p.rank && k < k1;
+                    cp_async16_or_zero(d + ZB + row * (kLrRound * 2) + 16 * (piece ^ (row & 7)),
+                                       in ? w + static_cast<size_t>(r0 + row) * p.cols + k : w, in);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.f;
+    const int live = tile.len - 32 * th;  // tokens of this warp (maybe none)
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) stage(k0 + i * kLrRound, i);
+    int buf = 0;
+    for (int kb = k0; kb < k1; kb += kLrRound) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();  // this round is there, and the stage read last is free
+        stage(kb + (kStages - 1) * kLrRound, buf == 0 ? kStages - 1 : buf - 1);
+        const uint32_t zs = base + buf * STAGE, ws = zs + ZB;
+        buf = buf + 1 == kStages ? 0 : buf + 1;
+        if (live > 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 16 columns each: pieces 4 kq + 2 h, + 1
+                unsigned a[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (kTrans) {
+                        ldsm_t4(a[m], ws + (32 * kq + 16 * h + 8 * (lane >> 4) + (lane & 7)) * ROW + 32 * m + 16 * ((lane >> 3) & 1));
+                    } else {
+                        const int row = 16 * m + (lane & 15), piece = 4 * kq + 2 * h + (lane >> 4);
+                        ldsm_4(a[m], ws + row * (kLrRound * 2) + 16 * (piece ^ (row & 7)));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NT; i += 2) {
+                    if (8 * i >= live) break;
+                    unsigned b[4];
+                    const int row = 32 * th + 8 * i + 8 * (lane >> 4) + (lane & 7), piece = 4 * kq + 2 * h + ((lane >> 3) & 1);
+                    ldsm_4(b, zs + row * (kLrRound * 2) + 16 * (piece ^ (row & 7)));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        lr_mma(acc[m][i], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+                        lr_mma(acc[m][i + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+                    }
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // the stages become the reduction's
 
     // the column warps' sums, in order
     float* red = reinterpret_cast<float*>(smem);
     constexpr int V = MT * NT * 4;
     if (kq > 0) {
-        float* d = red + ((kq - 1) * (kSmall ? 1 : 2) + th) * V * 32 + lane;
+        float* d = red + ((kq - 1) * 2 + th) * V * 32 + lane;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -393,9 +581,10 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constan
                 for (int e = 0; e < 4; ++e) d[((m * NT + i) * 4 + e) * 32] = acc[m][i][e];
     }
     __syncthreads();
-    if (kq > 0) return;
-    for (int k = 1; k < KW; ++k) {
-        const float* d = red + ((k - 1) * (kSmall ? 1 : 2) + th) * V * 32 + lane;
+    if (kq > 0 || live <= 0) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const float* d = red + (k * 2 + th) * V * 32 + lane;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -410,7 +599,7 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constan
         for (int e = 0; e < 2; ++e) {
             const int t = 32 * th + 8 * i + 2 * q + e;
             if (t >= tile.len) continue;
-            float* row = out + static_cast<size_t>(p.order[tile.first + t]) * p.rank;
+            float* row = out + static_cast<size_t>(s_tok[t]) * p.rank;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -421,11 +610,11 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constan
         }
 }
 
-__host__ __device__ constexpr size_t lr_down_smem(int mt, bool small, bool trans) {
-    const size_t kw = small ? 8 : 4, nt = small ? 1 : 4;
-    const size_t red = (kw - 1) * (small ? 1 : 2) * mt * nt * 4 * 32 * 4;
-    const size_t stage = trans ? 2 * 32 * kw * (static_cast<size_t>(mt) * 32 + 16) : 0;
-    return red > stage ? red : stage;
+__host__ __device__ constexpr size_t lr_down_smem(int mt, bool trans) {
+    const size_t red = size_t{3} * 2 * mt * 16 * 32 * 4;
+    const size_t stages = lr_down_stages(mt) * (size_t{kLrTile} * kLrRound * 2 + (trans ? kLrRound * (static_cast<size_t>(mt) * 32 + 16)
+                                                                              : static_cast<size_t>(mt) * 16 * kLrRound * 2));
+    return red > stages ? red : stages;
 }
 
 // ------------------------------------------------------------------ out = base + W w
@@ -433,36 +622,57 @@ struct LrUpParams {
     const int32_t* head;
     const int32_t* order;
     const LrTile* tiles;
+    const int32_t* slots;
     const float* part;      // [splits][tokens][rank]
     const float* scale;
     const uint16_t* w;      // [n][cols][rank], or [n][rank][cols] (kTrans)
     const uint16_t* base;   // [tokens][cols] or NULL
     uint16_t* out;          // [tokens][cols]
     float* sum;             // [tokens][rank]: the sum of the parts, or NULL
-    int32_t tokens, cols, rank;
+    int32_t tokens, cols, rank, n;
     int32_t splits;
-    int32_t range;          // columns a CTA, a multiple of 128
+    int32_t range;          // columns a CTA, a multiple of 64
 };
 
-template <bool kTrans>
+// base [16 KT_TOKENS][64 columns] and the weights of the same 64 columns come
+// through shared memory, three steps deep; the factors w stay in registers.
+// kSmall: 8 tokens, the four warps along the columns; else a warp has 16 of
+// the 64 tokens.  KS: 16-rank steps.
+constexpr int kLrUpCols = 64;
+constexpr int kLrUpStages = 3;
+
+template <int KS, bool kSmall, bool kTrans>
 __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ LrUpParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    uint4* s_w = reinterpret_cast<uint4*>(smem);  // [token tile of 16][16 ranks][high | low][lane]
-    __shared__ int s_tok[kLrTile];
+    constexpr int NT = kSmall ? 2 : 8;              // 8-column tiles a warp
+    constexpr int ROWS = kSmall ? kLrSmallTile : kLrTile;
+    constexpr int BB = ROWS * kLrUpCols * 2;        // 16-byte pieces xored with the row
+    constexpr int WROW = kTrans ? kLrUpCols * 2 : KS * 32 + 16;  // (kTrans) xored with the row, else padded
+    constexpr int WB = (kTrans ? KS * 16 : kLrUpCols) * WROW;
+    constexpr int STAGE = BB + WB;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ LrSmall s_small;
+    __shared__ int s_rows[kLrTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
     pdl_wait();
     pdl_launch_dependents();
-    if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
-    const LrTile tile = p.tiles[blockIdx.x];
+    LrTile tile;
+    if (kSmall) {
+        tile = lr_find_tile(s_small, p.slots, p.tokens, p.n, blockIdx.x);
+        if (tile.len == 0) return;
+    } else {
+        if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
+        tile = p.tiles[blockIdx.x];
+        if (tid < tile.len) s_rows[tid] = p.order[tile.first + tid];
+        __syncthreads();
+    }
+    const int* s_tok = kSmall ? s_small.tok : s_rows;
     const int c0 = static_cast<int>(blockIdx.y) * p.range, c1 = min(p.cols, c0 + p.range);
-    for (int i = tid; i < tile.len; i += kLrUpThreads) s_tok[i] = p.order[tile.first + i];
-    __syncthreads();
-    const int per_row = (c1 - c0) >> 3;
     if (tile.slot < 0) {  // tokens without an adapter
         if (p.sum && blockIdx.y == 0)
             for (int i = tid; i < tile.len * p.rank; i += kLrUpThreads)
                 p.sum[static_cast<size_t>(s_tok[i / p.rank]) * p.rank + i % p.rank] = 0.f;
         if (p.base == p.out) return;
+        const int per_row = (c1 - c0) >> 3;
         for (int i = tid; i < tile.len * per_row; i += kLrUpThreads) {
             const int t = i / per_row;
             const size_t at = static_cast<size_t>(s_tok[t]) * p.cols + c0 + 8 * (i - t * per_row);
@@ -471,108 +681,124 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
         }
         return;
     }
-    // A operands: lane (c, q) holds tokens c and c + 8, ranks 4q..4q+3 of every 16
-    const int mt = (tile.len + 15) >> 4, ks = (p.rank + 15) >> 4;
-    const float s = __ldg(p.scale + tile.slot);
-    for (int i = warp; i < mt * ks; i += kLrUpThreads / 32) {
-        const int m = i / ks, r = 16 * (i - m * ks) + 4 * q;
-        unsigned hi[4], lo[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = 16 * m + 8 * h + c;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t < tile.len && r < p.rank) {
-                const size_t at = static_cast<size_t>(s_tok[t]) * p.rank + r;
-                f = *reinterpret_cast<const float4*>(p.part + at);
-                for (int k = 1; k < p.splits; ++k) {
-                    const float4 g = *reinterpret_cast<const float4*>(p.part + static_cast<size_t>(k) * p.tokens * p.rank + at);
-                    f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
-                }
-                if (p.sum && blockIdx.y == 0) *reinterpret_cast<float4*>(p.sum + at) = f;
-            }
-            lr_split2(s * f.x, s * f.y, hi[h], lo[h]);
-            lr_split2(s * f.z, s * f.w, hi[2 + h], lo[2 + h]);
-        }
-        s_w[(2 * i) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        s_w[(2 * i + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-    __syncthreads();
-
     const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int col = c0 + 32 * warp; col < c1; col += 32 * (kLrUpThreads / 32)) {
-        const bool col_on = col + 8 * q < c1;
-        uint4 base[4][2];
+    const uint32_t sbase = smem_addr(smem);
+    auto stage = [&](int col, int buf) {
+        const uint32_t d = sbase + buf * STAGE;
+        if (col < c1) {
+            const int piece = tid & 7, k = col + 8 * piece;
+            if (p.base)
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+                for (int row = tid >> 3; row < ROWS; row += kLrUpThreads / 8) {
+                    const bool in = row < tile.len && k < c1;
+                    cp_async16_or_zero(d + row * (kLrUpCols * 2) + 16 * (piece ^ (row & 7)),
+                                       in ? p.base + static_cast<size_t>(s_tok[row]) * p.cols + k : p.base, in);
+                }
+            if (kTrans) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = 16 * m + 8 * h + c;
-                base[m][h] = zero;
-                if (p.base && col_on && t < tile.len)
-                    base[m][h] = *reinterpret_cast<const uint4*>(p.base + static_cast<size_t>(s_tok[t]) * p.cols + col + 8 * q);
-            }
-        float acc[4][4][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-        for (int k = 0; k < ks; ++k) {
-            const int r = 16 * k + 4 * q;
-            unsigned b[4][2];  // MMA tile j, its column c: column 8 (c / 2) + 2 j + c % 2 of the chunk
-            if (!kTrans) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = col + 8 * (c >> 1) + 2 * j + (c & 1);
-                    uint2 v = make_uint2(0, 0);
-                    if (n < c1 && r < p.rank) v = __ldg(reinterpret_cast<const uint2*>(w + static_cast<size_t>(n) * p.rank + r));
-                    b[j][0] = v.x;
-                    b[j][1] = v.y;
+                for (int row = tid >> 3; row < KS * 16; row += kLrUpThreads / 8) {
+                    const bool in = row < p.rank && k < c1;
+                    cp_async16_or_zero(d + BB + row * WROW + 16 * (piece ^ (row & 7)),
+                                       in ? w + static_cast<size_t>(row) * p.cols + k : w, in);
                 }
             } else {
-                uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = (r < p.rank && col + 8 * (c >> 1) < c1)
-                               ? __ldg(reinterpret_cast<const uint4*>(w + static_cast<size_t>(r + i) * p.cols + col + 8 * (c >> 1)))
-                               : zero;
-                const unsigned sel = (c & 1) ? 0x7632u : 0x5410u;
-                b[0][0] = prmt(v[0].x, v[1].x, sel); b[0][1] = prmt(v[2].x, v[3].x, sel);
-                b[1][0] = prmt(v[0].y, v[1].y, sel); b[1][1] = prmt(v[2].y, v[3].y, sel);
-                b[2][0] = prmt(v[0].z, v[1].z, sel); b[2][1] = prmt(v[2].z, v[3].z, sel);
-                b[3][0] = prmt(v[0].w, v[1].w, sel); b[3][1] = prmt(v[2].w, v[3].w, sel);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if (m >= mt) break;
-                const uint4 h = s_w[2 * (m * ks + k) * 32 + lane], l = s_w[(2 * (m * ks + k) + 1) * 32 + lane];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    lr_mma(acc[m][j], h.x, h.y, h.z, h.w, b[j][0], b[j][1]);
-                    lr_mma(acc[m][j], l.x, l.y, l.z, l.w, b[j][0], b[j][1]);
+                for (int i = tid; i < kLrUpCols * 2 * KS; i += kLrUpThreads) {
+                    const int n = i / (2 * KS), pc = i - n * 2 * KS;
+                    const bool in = col + n < c1 && 8 * pc < p.rank;
+                    cp_async16_or_zero(d + BB + n * WROW + 16 * pc, in ? w + static_cast<size_t>(col + n) * p.rank + 8 * pc : w, in);
                 }
             }
         }
+        cp_async_commit();
+    };
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+    for (int i = 0; i < kLrUpStages - 1; ++i) stage(c0 + i * kLrUpCols, i);
+
+    // A operands: lane (c, q) holds tokens c and c + 8 of the warp's 16, ranks 16 k + 2q, + 1, + 8, + 9
+    unsigned hi[KS][4], lo[KS][4];
+    const int m0 = kSmall ? 0 : 16 * warp;
+    const float s = __ldg(p.scale + tile.slot);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = 16 * m + 8 * h + c;
-                if (t >= tile.len || !col_on) continue;
-                const unsigned bw[4] = {base[m][h].x, base[m][h].y, base[m][h].z, base[m][h].w};
-                unsigned o[4];
+    for (int k = 0; k < KS; ++k)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[j] = lr_pack(lr_lo(bw[j]) + acc[m][j][2 * h], lr_hi(bw[j]) + acc[m][j][2 * h + 1]);
-                *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(s_tok[t]) * p.cols + col + 8 * q) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
+        for (int e = 0; e < 4; ++e) {
+            const int t = m0 + 8 * (e & 1) + c, r = 16 * k + 8 * (e >> 1) + 2 * q;
+            float2 f = make_float2(0.f, 0.f);
+            if (t < tile.len && r < p.rank) {
+                const size_t at = static_cast<size_t>(s_tok[t]) * p.rank + r;
+                f = *reinterpret_cast<const float2*>(p.part + at);
+#pragma unroll 4
+                for (int i = 1; i < p.splits; ++i) {
+                    const float2 g = *reinterpret_cast<const float2*>(p.part + static_cast<size_t>(i) * p.tokens * p.rank + at);
+                    f.x += g.x;
+                    f.y += g.y;
+                }
+                if (p.sum && blockIdx.y == 0 && (!kSmall || warp == 0)) *reinterpret_cast<float2*>(p.sum + at) = f;
             }
+            lr_split2(s * f.x, s * f.y, hi[k][e], lo[k][e]);
+        }
+
+    int buf = 0;
+    for (int col = c0; col < c1; col += kLrUpCols) {
+        cp_async_wait<kLrUpStages - 2>();
+        __syncthreads();  // this step is there, and the stage stored last is free
+        stage(col + (kLrUpStages - 1) * kLrUpCols, buf == 0 ? kLrUpStages - 1 : buf - 1);
+        const uint32_t bs = sbase + buf * STAGE, ws = bs + BB;
+        unsigned char* tile_mem = smem + buf * STAGE;
+        buf = buf + 1 == kLrUpStages ? 0 : buf + 1;
+        if (m0 < tile.len) {
+            float acc[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+            const int j0 = kSmall ? 2 * warp : 0;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {  // columns 8 (j0 + j) .. + 15
+                    unsigned b[4];
+                    if (kTrans) {
+                        const int row = 16 * k + 8 * ((lane >> 3) & 1) + (lane & 7), piece = j0 + j + (lane >> 4);
+                        ldsm_t4(b, ws + row * WROW + 16 * (piece ^ (row & 7)));
+                    } else {
+                        ldsm_4(b, ws + (8 * (j0 + j) + 8 * (lane >> 4) + (lane & 7)) * WROW + 32 * k + 16 * ((lane >> 3) & 1));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        lr_mma(acc[j + i], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[2 * i], b[2 * i + 1]);
+                        lr_mma(acc[j + i], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[2 * i], b[2 * i + 1]);
+                    }
+                }
+            // base + result, in place of base
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int h = 0; h < (kSmall ? 1 : 2); ++h) {
+                    const int row = m0 + 8 * h + c;
+                    unsigned* at = reinterpret_cast<unsigned*>(tile_mem + row * (kLrUpCols * 2) + 16 * ((j0 + j) ^ (row & 7)) + 4 * q);
+                    const unsigned b = p.base ? *at : 0u;
+                    *at = lr_pack(lr_lo(b) + acc[j][2 * h], lr_hi(b) + acc[j][2 * h + 1]);
+                }
+        }
+        if (kSmall) __syncthreads();
+        else __syncwarp();
+        // whole rows out: kSmall 8 rows by 64 threads, else a warp's own 16 rows
+#pragma unroll
+        for (int i = kSmall ? tid : lane; i < (kSmall ? 64 : 128); i += kSmall ? kLrUpThreads : 32) {
+            const int row = m0 + (i >> 3), piece = i & 7, k = col + 8 * piece;
+            if (row < tile.len && k < c1)
+                *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(s_tok[row]) * p.cols + k) =
+                    *reinterpret_cast<const uint4*>(tile_mem + row * (kLrUpCols * 2) + 16 * (piece ^ (row & 7)));
+        }
     }
 }
 
-__host__ __device__ constexpr size_t lr_up_smem(int rank) { return size_t{4} * ((rank + 15) / 16) * 2 * 32 * 16; }
+__host__ __device__ constexpr size_t lr_up_smem(int ks, bool small, bool trans) {
+    return kLrUpStages * (size_t(small ? kLrSmallTile : kLrTile) * kLrUpCols * 2 +
+                          (trans ? size_t(ks) * 16 * kLrUpCols * 2 : size_t{kLrUpCols} * (size_t(ks) * 32 + 16)));
+}
 
 // ------------------------------------------------------------------ backward: the factors in two bf16 parts
 struct LrSplitParams {
