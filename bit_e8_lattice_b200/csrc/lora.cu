@@ -16,6 +16,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct LrGeom {
     int tile, mt;            // tokens a tile; 16-row tiles of the rank in a k_lr_down CTA
     int64_t tiles;           // most tiles
+    int64_t halves;          // about as many parts of 64 tokens (small batches: tiles)
     int64_t zparts;          // rank parts of k_lr_down
     int64_t unit, units, parts;  // tokens a unit, most units, most partial sums (backward)
 };
@@ -25,6 +26,7 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
     g.tile = tokens <= kLrSmallTokens ? kLrSmallTile : kLrTile;
     // every group (the tokens without an adapter are one) adds at most one tile that is not full
     g.tiles = std::min(tokens, ceil_div(tokens, g.tile) + std::min<int64_t>(tokens, int64_t{a.n} + 1));
+    g.halves = g.tile == kLrSmallTile ? g.tiles : std::min(tokens, ceil_div(tokens, kLrHalf) + std::min<int64_t>(tokens, int64_t{a.n} + 1));
     g.mt = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
     g.zparts = ceil_div(a.rank, 64);
     const int64_t along = ceil_div(a.rows, kLrGradCols) + ceil_div(a.cols, kLrGradCols);
@@ -34,12 +36,13 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
     return g;
 }
 
-// Columns a CTA of k_lr_down: as many as let all CTAs run at once, two an SM
-// (a second wave would wait for the first), at most 4,096 so that a warp's sum
-// has at most 64 MMAs.
+// Columns a CTA of k_lr_down: as many as let all CTAs run at once (a second
+// wave would wait for the first), at most 4,096 so that a warp's sum has at
+// most 64 MMAs.  In small batches four CTAs fit an SM and each has little to do.
 int64_t down_columns(const LrGeom& g, int64_t cols) {
     const int64_t least = ceil_div(cols, 4096), most = ceil_div(cols, 256);
-    const int64_t splits = std::min(most, std::max(least, 2 * 148 / (g.tiles * g.zparts)));
+    const int64_t at_once = 148 * (g.tile == kLrSmallTile ? 4 : 2);
+    const int64_t splits = std::min(most, std::max(least, at_once / (g.halves * g.zparts)));
     return ceil_div(ceil_div(cols, splits), 256) * 256;
 }
 
@@ -97,8 +100,8 @@ e8q_status allow_down() {
 
 template <int KS, bool kTrans>
 e8q_status allow_up() {
-    e8q_status st = allow(k_lr_up<KS, false, kTrans>, lr_up_smem(KS, false, kTrans));
-    return st == E8Q_OK ? allow(k_lr_up<KS, true, kTrans>, lr_up_smem(KS, true, kTrans)) : st;
+    e8q_status st = allow(k_lr_up<KS, kLrHalf, kTrans>, lr_up_smem(KS, kLrHalf, kTrans));
+    return st == E8Q_OK ? allow(k_lr_up<KS, kLrSmallTile, kTrans>, lr_up_smem(KS, kLrSmallTile, kTrans)) : st;
 }
 
 template <bool kTrans>
@@ -166,12 +169,13 @@ e8q_status launch_down(const e8q_adapters& a, const int32_t* slots, const void* 
     p.cols = static_cast<int32_t>(cols);
     p.rank = a.rank;
     p.per = static_cast<int32_t>(down_columns(g, cols));
-    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.per)), static_cast<unsigned>(g.zparts));
+    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.per)),
+                    static_cast<unsigned>(g.zparts * (g.tile == kLrSmallTile ? 1 : 2)));
     if (g.tile == kLrSmallTile) {
         const size_t smem = lr_down_few_smem(g.mt, kTrans);
-        if (g.mt == 1) return launch_pdl(k_lr_down_few<1, kTrans>, grid, kLrDownThreads, smem, s, p, overlaps);
-        if (g.mt == 2) return launch_pdl(k_lr_down_few<2, kTrans>, grid, kLrDownThreads, smem, s, p, overlaps);
-        return launch_pdl(k_lr_down_few<4, kTrans>, grid, kLrDownThreads, smem, s, p, overlaps);
+        if (g.mt == 1) return launch_pdl(k_lr_down_few<1, kTrans>, grid, kLrFewThreads, smem, s, p, overlaps);
+        if (g.mt == 2) return launch_pdl(k_lr_down_few<2, kTrans>, grid, kLrFewThreads, smem, s, p, overlaps);
+        return launch_pdl(k_lr_down_few<4, kTrans>, grid, kLrFewThreads, smem, s, p, overlaps);
     }
     const size_t smem = lr_down_smem(g.mt, kTrans);
     if (g.mt == 1) return launch_pdl(k_lr_down<1, kTrans>, grid, kLrDownThreads, smem, s, p);
@@ -180,9 +184,15 @@ e8q_status launch_down(const e8q_adapters& a, const int32_t* slots, const void* 
 }
 
 template <int KS, bool kTrans>
-e8q_status launch_up_rank(bool small, dim3 grid, cudaStream_t s, const LrUpParams& p) {
-    return small ? launch_pdl(k_lr_up<KS, true, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, true, kTrans), s, p)
-                 : launch_pdl(k_lr_up<KS, false, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, false, kTrans), s, p);
+e8q_status launch_up_rank(const LrGeom& g, cudaStream_t s, LrUpParams& p) {
+    const bool small = g.tile == kLrSmallTile;
+    // as long as all CTAs run at once (two an SM, four in small batches): many steps share the factors' preparation
+    const int64_t cols = lr_up_cols(small ? kLrSmallTile : kLrHalf);
+    const int64_t parts = std::min(std::max<int64_t>(1, (small ? 4 : 2) * 148 / g.halves), ceil_div(p.cols, cols));
+    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(parts), small ? 1 : 2);
+    constexpr int T = kLrHalf, S = kLrSmallTile;
+    return small ? launch_pdl(k_lr_up<KS, S, kTrans>, grid, lr_up_threads(S), lr_up_smem(KS, S, kTrans), s, p)
+                 : launch_pdl(k_lr_up<KS, T, kTrans>, grid, lr_up_threads(T), lr_up_smem(KS, T, kTrans), s, p);
 }
 
 template <bool kTrans>
@@ -204,15 +214,10 @@ e8q_status launch_up(const e8q_adapters& a, const int32_t* slots, const void* we
     p.cols = static_cast<int32_t>(cols);
     p.rank = a.rank;
     p.splits = static_cast<int32_t>(ceil_div(sum_cols, down_columns(g, sum_cols)));
-    // long ranges share the factors' preparation, short ones fill the GPU
-    p.range = static_cast<int32_t>(kLrUpCols);
-    while (p.range < 1024 && g.tiles * ceil_div(cols, 2 * p.range) >= kFill) p.range *= 2;
-    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.range)));
-    const bool small = g.tile == kLrSmallTile;
-    if (a.rank <= 16) return launch_up_rank<1, kTrans>(small, grid, s, p);
-    if (a.rank <= 32) return launch_up_rank<2, kTrans>(small, grid, s, p);
-    if (a.rank <= 64) return launch_up_rank<4, kTrans>(small, grid, s, p);
-    return launch_up_rank<8, kTrans>(small, grid, s, p);
+    if (a.rank <= 16) return launch_up_rank<1, kTrans>(g, s, p);
+    if (a.rank <= 32) return launch_up_rank<2, kTrans>(g, s, p);
+    if (a.rank <= 64) return launch_up_rank<4, kTrans>(g, s, p);
+    return launch_up_rank<8, kTrans>(g, s, p);
 }
 
 }  // namespace
@@ -322,10 +327,10 @@ e8q_status e8q_lora_backward(const e8q_adapters* a, const void* grad_y, const vo
         gp.n = a->n;
         gp.row_ctas = static_cast<int32_t>(ceil_div(a->rows, kLrGradCols));
         const dim3 grid(static_cast<unsigned>(g.units), static_cast<unsigned>(gp.row_ctas + ceil_div(a->cols, kLrGradCols)));
-        if (a->rank <= 16) st = launch_pdl(k_lr_grad<2>, grid, kLrGradThreads, lr_grad_smem(2), s, gp);
-        else if (a->rank <= 32) st = launch_pdl(k_lr_grad<4>, grid, kLrGradThreads, lr_grad_smem(4), s, gp);
-        else if (a->rank <= 64) st = launch_pdl(k_lr_grad<8>, grid, kLrGradThreads, lr_grad_smem(8), s, gp);
-        else st = launch_pdl(k_lr_grad<16>, grid, kLrGradThreads, lr_grad_smem(16), s, gp);
+        if (a->rank <= 16) st = launch_pdl(k_lr_grad<2>, grid, kLrGradCols, lr_grad_smem(2), s, gp);
+        else if (a->rank <= 32) st = launch_pdl(k_lr_grad<4>, grid, kLrGradCols, lr_grad_smem(4), s, gp);
+        else if (a->rank <= 64) st = launch_pdl(k_lr_grad<8>, grid, kLrGradCols, lr_grad_smem(8), s, gp);
+        else st = launch_pdl(k_lr_grad<16>, grid, kLrGradCols, lr_grad_smem(16), s, gp);
         const int64_t quads = (a->rows + a->cols) * (a->rank / 4);
         const dim3 jgrid(static_cast<unsigned>(std::min<int64_t>(ceil_div(quads, 256), kFill)), static_cast<unsigned>(a->n));
         if (st == E8Q_OK) st = launch_pdl(k_lr_join, jgrid, 256, 0, s, gp);

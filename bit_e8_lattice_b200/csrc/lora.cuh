@@ -40,13 +40,11 @@ constexpr int kLrMaxAdapters = 2048;
 constexpr int kLrMaxRank = 128;
 constexpr int64_t kLrMaxWidth = 1 << 20;
 constexpr int kLrPlanThreads = 1024;
-constexpr int kLrTile = 64;        // tokens a tile
+constexpr int kLrTile = 128;       // tokens a tile
 constexpr int kLrSmallTile = 8;    // in batches of up to kLrSmallTokens
 constexpr int kLrSmallTokens = 128;
+constexpr int kLrFewThreads = 256;
 constexpr int kLrDownThreads = 256;
-constexpr int kLrUpThreads = 128;
-constexpr int kLrGradThreads = 256;
-constexpr int kLrGradCols = 256;
 
 struct LrTile {  // of tokens of one adapter, in the grouped order
     int32_t first, len, slot, pad;
@@ -66,7 +64,7 @@ struct LrPlanParams {
 
 // One CTA: a stable counting sort by adapter, each warp over its own range.
 __global__ void __launch_bounds__(kLrPlanThreads) k_lr_plan(const __grid_constant__ LrPlanParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nb = p.n + 1;  // bin n: no adapter
     int* s_tok = reinterpret_cast<int*>(smem);   // [nb + 1] first token, tile, unit of each bin
@@ -324,10 +322,10 @@ __device__ __forceinline__ int lr_stage_row(int n) { return 16 * ((n >> 2) & 1) 
 // straight from global memory in 16-byte loads.  MT: 16-row tiles of the
 // rank (4 at most: higher ranks in gridDim.z parts).
 template <int MT, bool kTrans>
-__global__ void __launch_bounds__(kLrDownThreads) k_lr_down_few(const __grid_constant__ LrDownParams p) {
+__global__ void __launch_bounds__(kLrFewThreads) k_lr_down_few(const __grid_constant__ LrDownParams p) {
     constexpr int KW = 8, STEP = 32 * KW;   // columns a round
     constexpr int ROW = MT * 16 * 2 + 16;   // bytes of a staged row (kTrans), padded against bank conflicts
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     __shared__ LrSmall s_small;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
     pdl_wait();
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down_few(const __grid_con
         constexpr int CH = 2 * MT;  // 16-byte pieces of a row
         const uint32_t base = smem_addr(smem);
         auto stage = [&](int kb, int buf) {
-            for (int i = tid; i < STEP * CH; i += kLrDownThreads) {
+            for (int i = tid; i < STEP * CH; i += kLrFewThreads) {
                 const int n = i / CH, piece = i - n * CH, k = kb + n, r = r0 + 8 * piece;
                 const uint32_t dst = base + (buf * STEP + (n & ~31) + lr_stage_row(n & 31)) * ROW + 16 * piece;
                 const bool in = k < k1 && r < p.rank;
@@ -453,31 +451,39 @@ __host__ __device__ constexpr size_t lr_down_few_smem(int mt, bool trans) {
     return red > stage ? red : stage;
 }
 
-// Tiles of up to 64 tokens: z [64][128 columns] and the weights of the same
+// Half a tile, up to 64 tokens: z [64][128 columns] and the weights of the same
 // columns come through shared memory, three or four rounds deep (two CTAs an
-// SM: a round's compute is short, and the loads of the next ones have to be out).  8 warps: 4 along the
-// round's columns, 2 along the tokens.
+// SM: a round's compute is short, and the loads of the next ones have to be
+// out).  8 warps: 4 along the round's columns, 2 along the tokens.
 constexpr int kLrRound = 128;
+constexpr int kLrHalf = 64;
 __host__ __device__ constexpr int lr_down_stages(int mt) { return mt == 4 ? 3 : 4; }
+
+// The half of a tile that a CTA works on; len <= 0: none.
+__device__ __forceinline__ LrTile lr_half(LrTile t, int half) {
+    t.first += kLrHalf * half;
+    t.len = min(t.len - kLrHalf * half, kLrHalf);
+    return t;
+}
 
 template <int MT, bool kTrans>
 __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constant__ LrDownParams p) {
     constexpr int NT = 4, kStages = lr_down_stages(MT);
-    constexpr int ZB = kLrTile * kLrRound * 2;                           // 16-byte pieces xored with the row
+    constexpr int ZB = kLrHalf * kLrRound * 2;                           // 16-byte pieces xored with the row
     constexpr int ROW = MT * 16 * 2 + 16;                                // staged row (kTrans), padded
     constexpr int WB = kTrans ? kLrRound * ROW : MT * 16 * kLrRound * 2;  // (else) pieces xored with the row
     constexpr int STAGE = ZB + WB;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int s_tok[kLrTile];
+    __shared__ int s_tok[kLrHalf];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
     const int kq = warp & 3, th = warp >> 2;
     pdl_wait();
     pdl_launch_dependents();
     if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
-    const LrTile tile = p.tiles[blockIdx.x];
-    if (tile.slot < 0) return;
+    const LrTile tile = lr_half(p.tiles[blockIdx.x], blockIdx.z & 1);
+    if (tile.slot < 0 || tile.len <= 0) return;
     const int k0 = static_cast<int>(blockIdx.y) * p.per, k1 = min(p.cols, k0 + p.per);
-    const int r0 = static_cast<int>(blockIdx.z) * 64;
+    const int r0 = static_cast<int>(blockIdx.z >> 1) * 64;
     const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
     if (tid < tile.len) s_tok[tid] = p.order[tile.first + tid];
     __syncthreads();
@@ -612,7 +618,7 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constan
 
 __host__ __device__ constexpr size_t lr_down_smem(int mt, bool trans) {
     const size_t red = size_t{3} * 2 * mt * 16 * 32 * 4;
-    const size_t stages = lr_down_stages(mt) * (size_t{kLrTile} * kLrRound * 2 + (trans ? kLrRound * (static_cast<size_t>(mt) * 32 + 16)
+    const size_t stages = lr_down_stages(mt) * (size_t{kLrHalf} * kLrRound * 2 + (trans ? kLrRound * (static_cast<size_t>(mt) * 32 + 16)
                                                                               : static_cast<size_t>(mt) * 16 * kLrRound * 2));
     return red > stages ? red : stages;
 }
@@ -631,27 +637,30 @@ struct LrUpParams {
     float* sum;             // [tokens][rank]: the sum of the parts, or NULL
     int32_t tokens, cols, rank, n;
     int32_t splits;
-    int32_t range;          // columns a CTA, a multiple of 64
 };
 
-// base [16 KT_TOKENS][64 columns] and the weights of the same 64 columns come
-// through shared memory, three steps deep; the factors w stay in registers.
-// kSmall: 8 tokens, the four warps along the columns; else a warp has 16 of
-// the 64 tokens.  KS: 16-rank steps.
-constexpr int kLrUpCols = 64;
+// base [tokens][COLS columns] and the weights of the same columns come through
+// shared memory, three steps deep; the factors w stay in registers.  TOK: 8
+// tokens (small batches; four warps along 64 columns), or half a tile of 64
+// (eight warps: four along the tokens, two along 128 columns).  KS: 16-rank
+// steps.
 constexpr int kLrUpStages = 3;
+__host__ __device__ constexpr int lr_up_threads(int tok) { return tok == kLrSmallTile ? 128 : 256; }
+__host__ __device__ constexpr int lr_up_cols(int tok) { return tok == kLrSmallTile ? 64 : 128; }
 
-template <int KS, bool kSmall, bool kTrans>
-__global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ LrUpParams p) {
+template <int KS, int TOK, bool kTrans>
+__global__ void __launch_bounds__(lr_up_threads(TOK)) k_lr_up(const __grid_constant__ LrUpParams p) {
+    constexpr bool kSmall = TOK == kLrSmallTile;
+    constexpr int kThreads = lr_up_threads(TOK), kStages = kLrUpStages, COLS = lr_up_cols(TOK);
     constexpr int NT = kSmall ? 2 : 8;              // 8-column tiles a warp
-    constexpr int ROWS = kSmall ? kLrSmallTile : kLrTile;
-    constexpr int BB = ROWS * kLrUpCols * 2;        // 16-byte pieces xored with the row
-    constexpr int WROW = kTrans ? kLrUpCols * 2 : KS * 32 + 16;  // (kTrans) xored with the row, else padded
-    constexpr int WB = (kTrans ? KS * 16 : kLrUpCols) * WROW;
+    constexpr int ROWS = TOK;
+    constexpr int BB = ROWS * COLS * 2;        // 16-byte pieces xored with the row
+    constexpr int WROW = kTrans ? COLS * 2 : KS * 32 + 16;  // (kTrans) xored with the row, else padded
+    constexpr int WB = (kTrans ? KS * 16 : COLS) * WROW;
     constexpr int STAGE = BB + WB;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ LrSmall s_small;
-    __shared__ int s_rows[kLrTile];
+    __shared__ int s_rows[kLrHalf];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
     pdl_wait();
     pdl_launch_dependents();
@@ -661,49 +670,79 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
         if (tile.len == 0) return;
     } else {
         if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
-        tile = p.tiles[blockIdx.x];
+        tile = lr_half(p.tiles[blockIdx.x], blockIdx.z);
+        if (tile.len <= 0) return;
         if (tid < tile.len) s_rows[tid] = p.order[tile.first + tid];
         __syncthreads();
     }
     const int* s_tok = kSmall ? s_small.tok : s_rows;
-    const int c0 = static_cast<int>(blockIdx.y) * p.range, c1 = min(p.cols, c0 + p.range);
+    // this CTA's steps: every gridDim.y-th, so that the CTAs of a tile work on neighbouring columns of its rows
+    const int c0 = static_cast<int>(blockIdx.y) * COLS, c1 = p.cols, next = static_cast<int>(gridDim.y) * COLS;
     if (tile.slot < 0) {  // tokens without an adapter
         if (p.sum && blockIdx.y == 0)
-            for (int i = tid; i < tile.len * p.rank; i += kLrUpThreads)
+            for (int i = tid; i < tile.len * p.rank; i += kThreads)
                 p.sum[static_cast<size_t>(s_tok[i / p.rank]) * p.rank + i % p.rank] = 0.f;
         if (p.base == p.out) return;
-        const int per_row = (c1 - c0) >> 3;
-        for (int i = tid; i < tile.len * per_row; i += kLrUpThreads) {
-            const int t = i / per_row;
-            const size_t at = static_cast<size_t>(s_tok[t]) * p.cols + c0 + 8 * (i - t * per_row);
-            *reinterpret_cast<uint4*>(p.out + at) =
-                p.base ? *reinterpret_cast<const uint4*>(p.base + at) : make_uint4(0, 0, 0, 0);
+        // copied, the loads of two steps out before their stores
+        constexpr int AT_ONCE = kThreads / (COLS / 8), R = (ROWS + AT_ONCE - 1) / AT_ONCE;
+        const int mine = 8 * (tid % (COLS / 8)), first = tid / (COLS / 8);
+        for (int col = c0 + mine; col < c1; col += 2 * next) {
+            uint4 v[2][R];
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int row = first + AT_ONCE * i, k = col + d * next;
+                    v[d][i] = make_uint4(0, 0, 0, 0);
+                    if (p.base && row < tile.len && k < c1)
+                        v[d][i] = *reinterpret_cast<const uint4*>(p.base + static_cast<size_t>(s_tok[row]) * p.cols + k);
+                }
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int row = first + AT_ONCE * i, k = col + d * next;
+                    if (row < tile.len && k < c1)
+                        *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(s_tok[row]) * p.cols + k) = v[d][i];
+                }
         }
         return;
     }
     const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
     const uint32_t sbase = smem_addr(smem);
+    const int m0 = kSmall ? 0 : 16 * (warp & 3), j0 = kSmall ? 2 * warp : 8 * (warp >> 2);  // its tokens and column tiles
+    // this thread's rows of base and out: kSmall one, of 64 threads; else four of its warp's 16, in its warp's columns
+    constexpr int OWN = kSmall ? 1 : 4;
+    const int row0 = kSmall ? (tid >> 3) : m0 + (lane >> 3), piece = (kSmall ? 0 : j0) + (tid & 7);
+    long long off[OWN];  // their first element in this thread's column piece; negative: none
+    uint32_t own[OWN];   // their place in a stage
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int row = row0 + 4 * i;
+        off[i] = row < tile.len ? static_cast<long long>(s_tok[row]) * p.cols + 8 * piece : -1;
+        own[i] = row * (COLS * 2) + 16 * (piece ^ (row & 7));
+    }
     auto stage = [&](int col, int buf) {
         const uint32_t d = sbase + buf * STAGE;
         if (col < c1) {
-            const int piece = tid & 7, k = col + 8 * piece;
-            if (p.base)
+            const int k = col + 8 * piece;
+            if (p.base && (!kSmall || tid < 8 * ROWS))
 #pragma unroll
-                for (int row = tid >> 3; row < ROWS; row += kLrUpThreads / 8) {
-                    const bool in = row < tile.len && k < c1;
-                    cp_async16_or_zero(d + row * (kLrUpCols * 2) + 16 * (piece ^ (row & 7)),
-                                       in ? p.base + static_cast<size_t>(s_tok[row]) * p.cols + k : p.base, in);
+                for (int i = 0; i < OWN; ++i) {
+                    const bool in = off[i] >= 0 && k < c1;
+                    cp_async16_or_zero(d + own[i], in ? p.base + off[i] + col : p.base, in);
                 }
             if (kTrans) {
 #pragma unroll
-                for (int row = tid >> 3; row < KS * 16; row += kLrUpThreads / 8) {
-                    const bool in = row < p.rank && k < c1;
-                    cp_async16_or_zero(d + BB + row * WROW + 16 * (piece ^ (row & 7)),
-                                       in ? w + static_cast<size_t>(row) * p.cols + k : w, in);
+                for (int i = tid; i < KS * 16 * (COLS / 8); i += kThreads) {
+                    const int row = i / (COLS / 8), pc = i % (COLS / 8);
+                    const bool in = row < p.rank && col + 8 * pc < c1;
+                    cp_async16_or_zero(d + BB + row * WROW + 16 * (pc ^ (row & 7)),
+                                       in ? w + static_cast<size_t>(row) * p.cols + col + 8 * pc : w, in);
                 }
             } else {
 #pragma unroll
-                for (int i = tid; i < kLrUpCols * 2 * KS; i += kLrUpThreads) {
+                for (int i = tid; i < COLS * 2 * KS; i += kThreads) {
                     const int n = i / (2 * KS), pc = i - n * 2 * KS;
                     const bool in = col + n < c1 && 8 * pc < p.rank;
                     cp_async16_or_zero(d + BB + n * WROW + 16 * pc, in ? w + static_cast<size_t>(col + n) * p.rank + 8 * pc : w, in);
@@ -713,11 +752,10 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kLrUpStages - 1; ++i) stage(c0 + i * kLrUpCols, i);
+    for (int i = 0; i < kStages - 1; ++i) stage(c0 + i * next, i);
 
     // A operands: lane (c, q) holds tokens c and c + 8 of the warp's 16, ranks 16 k + 2q, + 1, + 8, + 9
     unsigned hi[KS][4], lo[KS][4];
-    const int m0 = kSmall ? 0 : 16 * warp;
     const float s = __ldg(p.scale + tile.slot);
 #pragma unroll
     for (int k = 0; k < KS; ++k)
@@ -734,70 +772,86 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
                     f.x += g.x;
                     f.y += g.y;
                 }
-                if (p.sum && blockIdx.y == 0 && (!kSmall || warp == 0)) *reinterpret_cast<float2*>(p.sum + at) = f;
+                if (p.sum && blockIdx.y == 0 && (kSmall ? warp == 0 : warp < 4)) *reinterpret_cast<float2*>(p.sum + at) = f;
             }
             lr_split2(s * f.x, s * f.y, hi[k][e], lo[k][e]);
         }
 
     int buf = 0;
-    for (int col = c0; col < c1; col += kLrUpCols) {
-        cp_async_wait<kLrUpStages - 2>();
+    for (int col = c0; col < c1; col += next) {
+        cp_async_wait<kStages - 2>();
         __syncthreads();  // this step is there, and the stage stored last is free
-        stage(col + (kLrUpStages - 1) * kLrUpCols, buf == 0 ? kLrUpStages - 1 : buf - 1);
+        stage(col + (kStages - 1) * next, buf == 0 ? kStages - 1 : buf - 1);
         const uint32_t bs = sbase + buf * STAGE, ws = bs + BB;
         unsigned char* tile_mem = smem + buf * STAGE;
-        buf = buf + 1 == kLrUpStages ? 0 : buf + 1;
+        unsigned char* mine = tile_mem + (m0 + c) * (COLS * 2) + 4 * q;  // rows m0 + c, + 8 (the same xor)
+        buf = buf + 1 == kStages ? 0 : buf + 1;
         if (m0 < tile.len) {
+            // the sums begin with base; the result takes its place in the stage
+            constexpr int H = kSmall ? 1 : 2;
             float acc[NT][4];
+            if (p.base) {
+                unsigned b[NT][2];
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-            const int j0 = kSmall ? 2 * warp : 0;
+                    for (int h = 0; h < H; ++h) b[j][h] = *reinterpret_cast<const unsigned*>(mine + h * 8 * (COLS * 2) + 16 * ((j0 + j) ^ c));
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+                for (int j = 0; j < NT; ++j) {
+                    acc[j][0] = lr_lo(b[j][0]);
+                    acc[j][1] = lr_hi(b[j][0]);
+                    acc[j][2] = kSmall ? 0.f : lr_lo(b[j][H - 1]);
+                    acc[j][3] = kSmall ? 0.f : lr_hi(b[j][H - 1]);
+                }
+            } else {
 #pragma unroll
-                for (int j = 0; j < NT; j += 2) {  // columns 8 (j0 + j) .. + 15
-                    unsigned b[4];
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                unsigned b[NT / 2][4];  // columns 8 (j0 + 2 i) .. + 15
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) {
                     if (kTrans) {
-                        const int row = 16 * k + 8 * ((lane >> 3) & 1) + (lane & 7), piece = j0 + j + (lane >> 4);
-                        ldsm_t4(b, ws + row * WROW + 16 * (piece ^ (row & 7)));
+                        const int row = 16 * k + 8 * ((lane >> 3) & 1) + (lane & 7), pc = j0 + 2 * i + (lane >> 4);
+                        ldsm_t4(b[i], ws + row * WROW + 16 * (pc ^ (row & 7)));
                     } else {
-                        ldsm_4(b, ws + (8 * (j0 + j) + 8 * (lane >> 4) + (lane & 7)) * WROW + 32 * k + 16 * ((lane >> 3) & 1));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        lr_mma(acc[j + i], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[2 * i], b[2 * i + 1]);
-                        lr_mma(acc[j + i], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[2 * i], b[2 * i + 1]);
+                        ldsm_4(b[i], ws + (8 * (j0 + 2 * i) + 8 * (lane >> 4) + (lane & 7)) * WROW + 32 * k + 16 * ((lane >> 3) & 1));
                     }
                 }
-            // base + result, in place of base
+                // high parts of all tiles, then low parts: MMAs on one accumulator lie NT apart
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    lr_mma(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    lr_mma(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
+            }
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int h = 0; h < (kSmall ? 1 : 2); ++h) {
-                    const int row = m0 + 8 * h + c;
-                    unsigned* at = reinterpret_cast<unsigned*>(tile_mem + row * (kLrUpCols * 2) + 16 * ((j0 + j) ^ (row & 7)) + 4 * q);
-                    const unsigned b = p.base ? *at : 0u;
-                    *at = lr_pack(lr_lo(b) + acc[j][2 * h], lr_hi(b) + acc[j][2 * h + 1]);
-                }
+                for (int h = 0; h < H; ++h)
+                    *reinterpret_cast<unsigned*>(mine + h * 8 * (COLS * 2) + 16 * ((j0 + j) ^ c)) =
+                        lr_pack(acc[j][2 * h], acc[j][2 * h + 1]);
         }
         if (kSmall) __syncthreads();
         else __syncwarp();
-        // whole rows out: kSmall 8 rows by 64 threads, else a warp's own 16 rows
+        if (!kSmall || tid < 8 * ROWS) {
+            uint4 o[OWN];
 #pragma unroll
-        for (int i = kSmall ? tid : lane; i < (kSmall ? 64 : 128); i += kSmall ? kLrUpThreads : 32) {
-            const int row = m0 + (i >> 3), piece = i & 7, k = col + 8 * piece;
-            if (row < tile.len && k < c1)
-                *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(s_tok[row]) * p.cols + k) =
-                    *reinterpret_cast<const uint4*>(tile_mem + row * (kLrUpCols * 2) + 16 * (piece ^ (row & 7)));
+            for (int i = 0; i < OWN; ++i) o[i] = *reinterpret_cast<const uint4*>(tile_mem + own[i]);
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                if (off[i] >= 0 && col + 8 * piece < c1) *reinterpret_cast<uint4*>(p.out + off[i] + col) = o[i];
         }
     }
 }
 
-__host__ __device__ constexpr size_t lr_up_smem(int ks, bool small, bool trans) {
-    return kLrUpStages * (size_t(small ? kLrSmallTile : kLrTile) * kLrUpCols * 2 +
-                          (trans ? size_t(ks) * 16 * kLrUpCols * 2 : size_t{kLrUpCols} * (size_t(ks) * 32 + 16)));
+__host__ __device__ constexpr size_t lr_up_smem(int ks, int tok, bool trans) {
+    return kLrUpStages * (size_t(tok) * lr_up_cols(tok) * 2 +
+                          (trans ? size_t(ks) * 16 * lr_up_cols(tok) * 2 : size_t(lr_up_cols(tok)) * (size_t(ks) * 32 + 16)));
 }
 
 // ------------------------------------------------------------------ backward: the factors in two bf16 parts
@@ -857,11 +911,14 @@ struct LrGradParams {
     int32_t row_ctas;       // CTAs along the rows of B; the rest take the columns of A
 };
 
+constexpr int kLrGradCols = 256;  // of a CTA, 32 a warp
+
 // NT: 8-wide tiles of the rank
 template <int NT>
-__global__ void __launch_bounds__(kLrGradThreads) k_lr_grad(const __grid_constant__ LrGradParams p) {
+__global__ void __launch_bounds__(kLrGradCols) k_lr_grad(const __grid_constant__ LrGradParams p) {
+    constexpr int kCols = kLrGradCols;                 // and threads
     constexpr int WROW = NT * 16 + 16;                 // bytes of a row of w, padded against bank conflicts
-    constexpr int ZBYTES = 64 * kLrGradCols * 2, WBYTES = 64 * WROW, STAGE = ZBYTES + 2 * WBYTES;
+    constexpr int ZBYTES = 64 * kCols * 2, WBYTES = 64 * WROW, STAGE = ZBYTES + 2 * WBYTES;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
     pdl_wait();
@@ -870,32 +927,44 @@ __global__ void __launch_bounds__(kLrGradThreads) k_lr_grad(const __grid_constan
     const LrTile unit = p.units[blockIdx.x];
     const bool is_b = static_cast<int>(blockIdx.y) < p.row_ctas;
     const int width = is_b ? p.rows : p.cols;
-    const int c0 = (is_b ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) - p.row_ctas) * kLrGradCols;
+    const int c0 = (is_b ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) - p.row_ctas) * kCols;
     const uint16_t* z = is_b ? p.gy : p.x;
     const size_t all = static_cast<size_t>(p.tokens) * p.rank;
     const uint16_t* wh = p.parts + (is_b ? 0 : 2 * all);
     const uint32_t base = smem_addr(smem);
 
-    // 64 tokens: z [64][256] (16-byte pieces xored with the row against bank conflicts), w high and low [64][rank]
+    // 64 tokens: z [64][kCols] (16-byte pieces xored with the row against bank conflicts), w high and low [64][rank]
+    constexpr int PIECES = kCols / 8, ROWS = kCols / PIECES;  // rows copied at once: 8
+    const int piece = tid % PIECES, row0 = tid / PIECES;
+    const bool col_on = c0 + 8 * piece < width;
+    const uint16_t* zc = z + c0 + 8 * piece;
+    int tok[64 / ROWS];  // of this thread's rows of the next stage (row0 + 8 i), loaded a stage ahead
+    auto tokens = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < 64 / ROWS; ++i) {
+            const int row = t0 + row0 + ROWS * i;
+            tok[i] = row < unit.len ? __ldg(p.order + unit.first + row) : -1;
+        }
+    };
     auto stage = [&](int t0, int buf) {
         const uint32_t d = base + buf * STAGE;
-        const int piece = tid & 31;
-        const bool col_on = c0 + 8 * piece < width;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = (tid >> 5) + 8 * i;
-            const bool on = col_on && t0 + row < unit.len;
-            const uint16_t* src = z;
-            if (on) src = z + static_cast<size_t>(p.order[unit.first + t0 + row]) * width + c0 + 8 * piece;
-            cp_async16_or_zero(d + row * (kLrGradCols * 2) + 16 * (piece ^ (row & 7)), src, on);
+        for (int i = 0; i < 64 / ROWS; ++i) {
+            const int row = row0 + ROWS * i;
+            const bool on = col_on && tok[i] >= 0;
+            cp_async16_or_zero(d + row * (kCols * 2) + 16 * (piece ^ (row & 7)),
+                               on ? zc + static_cast<size_t>(tok[i]) * width : z, on);
         }
-        for (int i = tid; i < 2 * 64 * NT; i += kLrGradThreads) {
-            const int half = i / (64 * NT), j = i - half * 64 * NT, row = j / NT, pc = j - row * NT;
-            const bool on = t0 + row < unit.len && 8 * pc < p.rank;
-            const uint16_t* src = wh;
-            if (on) src = wh + half * all + static_cast<size_t>(unit.first + t0 + row) * p.rank + 8 * pc;
-            cp_async16_or_zero(d + ZBYTES + half * WBYTES + row * WROW + 16 * pc, src, on);
-        }
+        tokens(t0 + 64);
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = tid; i < 64 * NT; i += kCols) {
+                const int row = i / NT, pc = i - row * NT;
+                const bool on = t0 + row < unit.len && 8 * pc < p.rank;
+                cp_async16_or_zero(d + ZBYTES + half * WBYTES + row * WROW + 16 * pc,
+                                   on ? wh + half * all + static_cast<size_t>(unit.first + t0 + row) * p.rank + 8 * pc : wh, on);
+            }
         cp_async_commit();
     };
 
@@ -906,6 +975,7 @@ __global__ void __launch_bounds__(kLrGradThreads) k_lr_grad(const __grid_constan
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+    tokens(0);
     stage(0, 0);
     int buf = 0;
     for (int t0 = 0; t0 < unit.len; t0 += 64, buf ^= 1) {
@@ -920,13 +990,13 @@ __global__ void __launch_bounds__(kLrGradThreads) k_lr_grad(const __grid_constan
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int piece = 4 * warp + 2 * m + ((lane >> 3) & 1);
-                ldsm_t4(a[m], zs + row * (kLrGradCols * 2) + 16 * (piece ^ (row & 7)));
+                ldsm_t4(a[m], zs + row * (kCols * 2) + 16 * (piece ^ (row & 7)));
             }
             const int wrow = 16 * k + 8 * ((lane >> 3) & 1) + (lane & 7);
 #pragma unroll
-            for (int j = 0; j < NT; j += 2) {
+            for (int half = 0; half < 2; ++half)  // high parts of all tiles, then low parts
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int j = 0; j < NT; j += 2) {
                     unsigned b[4];
                     ldsm_t4(b, ws + half * WBYTES + wrow * WROW + 16 * (j + (lane >> 4)));
 #pragma unroll
@@ -935,7 +1005,6 @@ __global__ void __launch_bounds__(kLrGradThreads) k_lr_grad(const __grid_constan
                         lr_mma(acc[m][j + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
                     }
                 }
-            }
         }
     }
     const bool whole = unit.pad < 0;  // the adapter's only unit

@@ -157,13 +157,13 @@ def _call(what: str, device: torch.device, stream, *args):
     """One library call on the device of its tensors: on `stream`, or on that
     device's current stream."""
     fn = getattr(lib(), what)
+    # (torch.cuda.current_stream() builds an object, which takes as long as a launch)
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream()
-        rc = fn(*args, s.cuda_stream)
+        rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream()
-            rc = fn(*args, s.cuda_stream)
+            rc = fn(*args, s)
     if rc != E8Q_OK:
         _check(rc, what)
 
@@ -572,6 +572,7 @@ class Lora:
         if self.max_tokens < 0:
             raise E8qError("max_tokens must not be negative")
         self._workspace = [None, None]
+        self._need = {}  # workspace bytes by (tokens, backward)
         self._buffers = {}
 
     def _c(self) -> AdaptersC:
@@ -579,7 +580,9 @@ class Lora:
                          self.rank)
 
     def _ws(self, ad: AdaptersC, tokens: int, backward: int) -> torch.Tensor:
-        need = lib().e8q_lora_workspace_bytes(ctypes.byref(ad), tokens, backward)
+        need = self._need.get((tokens, backward))
+        if need is None:
+            need = self._need[tokens, backward] = lib().e8q_lora_workspace_bytes(ctypes.byref(ad), tokens, backward)
         ws = self._workspace[backward]
         if ws is None or ws.numel() < need:
             need = max(need, lib().e8q_lora_workspace_bytes(ctypes.byref(ad), self.max_tokens, backward))
