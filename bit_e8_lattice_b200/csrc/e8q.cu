@@ -88,6 +88,9 @@ e8q_status ensure_device(int* dev_out) {
             }
             st = cuda_ok(cudaMemcpyToSymbol(g_gv_tab, words.data(), words.size() * sizeof(uint32_t)));
         }
+        if (st == E8Q_OK)
+            st = cuda_ok(cudaFuncSetAttribute(k_rb_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              static_cast<int>(kRbSortSmem)));
         // the row lookup of the widest rows holds more than the default 48 KB with its signs
         const int dr_smem = static_cast<int>(dr_smem_bytes(true, kMaxCols));
         if (st == E8Q_OK)
@@ -215,8 +218,7 @@ struct RbPlan {
     int64_t slices;      // of kRbSliceCols columns
     int64_t chunk;       // sorted tokens a summing CTA
     int64_t chunks;
-    int64_t radix_ctas;  // 0: no radix sort
-    size_t keys[2], order[2], hist, part;
+    size_t keys[2], order[2], part;
     size_t total;  // workspace; enough for fewer ids too
 };
 
@@ -244,12 +246,10 @@ RbPlan rb_plan(int64_t n, int64_t cols) {
         return o;
     };
     const bool radix = n > kRbRankMax;
-    r.radix_ctas = radix ? (n + kRbTile - 1) / kRbTile : 0;
     for (int i = 0; i < (radix ? 2 : 1); ++i) {
         r.keys[i] = take(static_cast<size_t>(n) * 4);
         r.order[i] = take(static_cast<size_t>(n) * 4);
     }
-    r.hist = take(static_cast<size_t>(r.radix_ctas) * kRbBins * 4);
     r.part = take(static_cast<size_t>(most) * 2 * cols * 4);
     r.total = at;
     return r;
@@ -818,27 +818,18 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
         int bits = 1;
         while ((int64_t{1} << bits) <= rows) ++bits;  // keys 0 .. rows
         const int passes = (bits + kRbDigitBits - 1) / kRbDigitBits, digit = (bits + passes - 1) / passes;
-        RbRadixParams r;
+        RbSortParams r;
         r.ids = q.ids;
         r.n = n;
-        r.hist = reinterpret_cast<uint32_t*>(w + pl.hist);
-        r.mask = (1 << digit) - 1;
-        const int grid = static_cast<int>(pl.radix_ctas);
-        for (int i = 0; i < passes && st == E8Q_OK; ++i) {
-            at = i & 1;
-            r.shift = i * digit;
-            r.keys_in = i ? reinterpret_cast<const int32_t*>(w + pl.keys[at ^ 1]) : nullptr;
-            r.order_in = i ? reinterpret_cast<const int32_t*>(w + pl.order[at ^ 1]) : nullptr;
-            r.keys = reinterpret_cast<int32_t*>(w + pl.keys[at]);
-            r.order = reinterpret_cast<int32_t*>(w + pl.order[at]);
-            if (i == 0) {
-                k_rb_hist<<<grid, 256, 0, s>>>(r);
-                st = cuda_ok(cudaGetLastError());
-            } else {
-                st = launch_pdl(k_rb_hist, grid, 256, 0, s, r);
-            }
-            if (st == E8Q_OK) st = launch_pdl(k_rb_scatter, grid, 256, 0, s, r);
+        r.passes = passes;
+        r.digit = digit;
+        for (int i = 0; i < 2; ++i) {
+            r.keys[i] = reinterpret_cast<int32_t*>(w + pl.keys[i]);
+            r.order[i] = reinterpret_cast<int32_t*>(w + pl.order[i]);
         }
+        k_rb_sort<<<kRbCluster, kRbSortThreads, kRbSortSmem, s>>>(r);
+        st = cuda_ok(cudaGetLastError());
+        at = (passes - 1) & 1;
     }
     if (st != E8Q_OK) return st;
     q.keys = reinterpret_cast<const int32_t*>(w + pl.keys[at]);
@@ -852,7 +843,7 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
     else if (lf) st = launch_pdl(k_rb_sum<false, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
     else st = launch_pdl(k_rb_sum<false, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
     if (st != E8Q_OK || pl.chunks == 1) return st;
-    const int64_t jgrid = (pl.chunks - 1) * ((cols + kRbJoinCols - 1) / kRbJoinCols);
+    const int64_t jgrid = (pl.chunks - 1) * pl.slices;
     if (jgrid > 0x7FFFFFFF) return E8Q_ERR_UNSUPPORTED;
     return lf ? launch_pdl(k_rb_join<true>, static_cast<int>(jgrid), kRbJoinThreads, 0, s, q)
               : launch_pdl(k_rb_join<false>, static_cast<int>(jgrid), kRbJoinThreads, 0, s, q);

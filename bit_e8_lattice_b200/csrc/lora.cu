@@ -9,7 +9,9 @@
 namespace e8q {
 namespace {
 
-constexpr int64_t kFill = 3 * 148;  // CTAs that fill the SMs; a constant, so that the order of the sums is the same on any device
+// CTAs that run at once where two fit an SM; a constant, so that the order of the
+// sums is the same on any device.
+constexpr int64_t kAtOnce = 2 * 148;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -30,7 +32,7 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
     g.mt = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
     g.zparts = ceil_div(a.rank, 64);
     const int64_t along = ceil_div(a.rows, kLrGradCols) + ceil_div(a.cols, kLrGradCols);
-    g.unit = ceil_div(ceil_div(tokens, std::max<int64_t>(1, kFill / along)), 64) * 64;
+    g.unit = ceil_div(ceil_div(tokens, std::max<int64_t>(1, kAtOnce / along)), 64) * 64;
     g.units = ceil_div(tokens, g.unit) + std::min<int64_t>(tokens, a.n);
     g.parts = 2 * ceil_div(tokens, g.unit);  // an adapter of several units has all but one full
     return g;
@@ -186,13 +188,13 @@ e8q_status launch_down(const e8q_adapters& a, const int32_t* slots, const void* 
 template <int KS, bool kTrans>
 e8q_status launch_up_rank(const LrGeom& g, cudaStream_t s, LrUpParams& p) {
     const bool small = g.tile == kLrSmallTile;
-    // as long as all CTAs run at once (two an SM, four in small batches): many steps share the factors' preparation
-    const int64_t cols = lr_up_cols(small ? kLrSmallTile : kLrHalf);
-    const int64_t parts = std::min(std::max<int64_t>(1, (small ? 4 : 2) * 148 / g.halves), ceil_div(p.cols, cols));
+    // two rounds of the four CTAs that an SM holds: enough steps to share the factors' preparation, and a short
+    // tail (one round: 5 % slower on a 4,096-token prefill)
+    const int64_t parts = std::min(std::max<int64_t>(1, 8 * 148 / g.halves), ceil_div(p.cols, kLrUpCols));
     const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(parts), small ? 1 : 2);
     constexpr int T = kLrHalf, S = kLrSmallTile;
-    return small ? launch_pdl(k_lr_up<KS, S, kTrans>, grid, lr_up_threads(S), lr_up_smem(KS, S, kTrans), s, p)
-                 : launch_pdl(k_lr_up<KS, T, kTrans>, grid, lr_up_threads(T), lr_up_smem(KS, T, kTrans), s, p);
+    return small ? launch_pdl(k_lr_up<KS, S, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, S, kTrans), s, p)
+                 : launch_pdl(k_lr_up<KS, T, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, T, kTrans), s, p);
 }
 
 template <bool kTrans>
@@ -307,7 +309,7 @@ e8q_status e8q_lora_backward(const e8q_adapters* a, const void* grad_y, const vo
         sp.tokens = static_cast<int32_t>(tokens);
         sp.rank = a->rank;
         sp.splits = static_cast<int32_t>(ceil_div(a->rows, down_columns(g, a->rows)));
-        st = launch_pdl(k_lr_split, static_cast<int>(std::min<int64_t>(kFill, ceil_div(tokens * (a->rank / 4), 256))), 256, 0, s, sp);
+        st = launch_pdl(k_lr_split, static_cast<int>(std::min<int64_t>(2 * kAtOnce, ceil_div(tokens * (a->rank / 4), 256))), 256, 0, s, sp);
         if (st != E8Q_OK) return st;
         LrGradParams gp;
         gp.head = sp.head;
@@ -332,7 +334,7 @@ e8q_status e8q_lora_backward(const e8q_adapters* a, const void* grad_y, const vo
         else if (a->rank <= 64) st = launch_pdl(k_lr_grad<8>, grid, kLrGradCols, lr_grad_smem(8), s, gp);
         else st = launch_pdl(k_lr_grad<16>, grid, kLrGradCols, lr_grad_smem(16), s, gp);
         const int64_t quads = (a->rows + a->cols) * (a->rank / 4);
-        const dim3 jgrid(static_cast<unsigned>(std::min<int64_t>(ceil_div(quads, 256), kFill)), static_cast<unsigned>(a->n));
+        const dim3 jgrid(static_cast<unsigned>(std::min<int64_t>(ceil_div(quads, 256), 2 * kAtOnce)), static_cast<unsigned>(a->n));
         if (st == E8Q_OK) st = launch_pdl(k_lr_join, jgrid, 256, 0, s, gp);
     }
     if (st == E8Q_OK && grad_x)

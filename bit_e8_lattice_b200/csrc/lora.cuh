@@ -639,19 +639,19 @@ struct LrUpParams {
     int32_t splits;
 };
 
-// base [tokens][COLS columns] and the weights of the same columns come through
+// base [tokens][64 columns] and the weights of the same columns come through
 // shared memory, three steps deep; the factors w stay in registers.  TOK: 8
-// tokens (small batches; four warps along 64 columns), or half a tile of 64
-// (eight warps: four along the tokens, two along 128 columns).  KS: 16-rank
-// steps.
-constexpr int kLrUpStages = 3;
-__host__ __device__ constexpr int lr_up_threads(int tok) { return tok == kLrSmallTile ? 128 : 256; }
-__host__ __device__ constexpr int lr_up_cols(int tok) { return tok == kLrSmallTile ? 64 : 128; }
+// tokens (small batches; four warps along the columns), or half a tile of 64
+// (four warps along the tokens).  Small CTAs, four an SM, because a step is a
+// chain of short waits (copies, barrier, ldmatrix, MMA, store) that only other
+// CTAs fill: 256 threads on 128 columns measured 4 % slower, tiles of 128
+// tokens 5 to 20 %.  KS: 16-rank steps.
+constexpr int kLrUpStages = 3, kLrUpThreads = 128, kLrUpCols = 64;
 
 template <int KS, int TOK, bool kTrans>
-__global__ void __launch_bounds__(lr_up_threads(TOK)) k_lr_up(const __grid_constant__ LrUpParams p) {
+__global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ LrUpParams p) {
     constexpr bool kSmall = TOK == kLrSmallTile;
-    constexpr int kThreads = lr_up_threads(TOK), kStages = kLrUpStages, COLS = lr_up_cols(TOK);
+    constexpr int kThreads = kLrUpThreads, kStages = kLrUpStages, COLS = kLrUpCols;
     constexpr int NT = kSmall ? 2 : 8;              // 8-column tiles a warp
     constexpr int ROWS = TOK;
     constexpr int BB = ROWS * COLS * 2;        // 16-byte pieces xored with the row
@@ -710,10 +710,10 @@ __global__ void __launch_bounds__(lr_up_threads(TOK)) k_lr_up(const __grid_const
     }
     const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
     const uint32_t sbase = smem_addr(smem);
-    const int m0 = kSmall ? 0 : 16 * (warp & 3), j0 = kSmall ? 2 * warp : 8 * (warp >> 2);  // its tokens and column tiles
-    // this thread's rows of base and out: kSmall one, of 64 threads; else four of its warp's 16, in its warp's columns
+    const int m0 = kSmall ? 0 : 16 * warp, j0 = kSmall ? 2 * warp : 0;  // the warp's tokens and column tiles
+    // this thread's rows of base and out: kSmall one, of 64 threads; else four of its warp's 16
     constexpr int OWN = kSmall ? 1 : 4;
-    const int row0 = kSmall ? (tid >> 3) : m0 + (lane >> 3), piece = (kSmall ? 0 : j0) + (tid & 7);
+    const int row0 = kSmall ? (tid >> 3) : m0 + (lane >> 3), piece = tid & 7;
     long long off[OWN];  // their first element in this thread's column piece; negative: none
     uint32_t own[OWN];   // their place in a stage
 #pragma unroll
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(lr_up_threads(TOK)) k_lr_up(const __grid_const
                     f.x += g.x;
                     f.y += g.y;
                 }
-                if (p.sum && blockIdx.y == 0 && (kSmall ? warp == 0 : warp < 4)) *reinterpret_cast<float2*>(p.sum + at) = f;
+                if (p.sum && blockIdx.y == 0 && (!kSmall || warp == 0)) *reinterpret_cast<float2*>(p.sum + at) = f;
             }
             lr_split2(s * f.x, s * f.y, hi[k][e], lo[k][e]);
         }
@@ -850,8 +850,8 @@ __global__ void __launch_bounds__(lr_up_threads(TOK)) k_lr_up(const __grid_const
 }
 
 __host__ __device__ constexpr size_t lr_up_smem(int ks, int tok, bool trans) {
-    return kLrUpStages * (size_t(tok) * lr_up_cols(tok) * 2 +
-                          (trans ? size_t(ks) * 16 * lr_up_cols(tok) * 2 : size_t(lr_up_cols(tok)) * (size_t(ks) * 32 + 16)));
+    return kLrUpStages * (size_t(tok) * kLrUpCols * 2 +
+                          (trans ? size_t(ks) * 16 * kLrUpCols * 2 : size_t(kLrUpCols) * (size_t(ks) * 32 + 16)));
 }
 
 // ------------------------------------------------------------------ backward: the factors in two bf16 parts

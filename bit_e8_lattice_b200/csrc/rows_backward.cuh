@@ -10,20 +10,19 @@
 //                     before it in (row, position) order, counted against all
 //                     n ids held in shared memory; n^2 comparisons over all
 //                     SMs cost less than the launches of a radix sort;
-//   above             k_rb_hist + k_rb_scatter a digit of up to 9 bits: each
-//                     CTA's histogram, then every CTA derives its own bases
-//                     from all histograms and places its keys in order.
+//   above             k_rb_sort: a stable radix sort by one cluster of CTAs.
 // Then
 //   k_rb_sum          one CTA per (chunk of sorted tokens, 1,024 columns): a
 //                     thread owns 8 columns and keeps a batch of rows in
-//                     flight.  A row whose tokens lie in one chunk is written at
-//                     once; a row cut by a chunk border leaves fp32 partial
-//                     sums (at most two a chunk).  Further CTAs of the same
-//                     launch write the zeros of the rows without a token, so
-//                     that every output byte is written once;
-//   k_rb_join         the rows cut by chunk borders: their partial sums in
-//                     order, the list split over 16 warps (a padding id may
-//                     fill thousands of chunks).
+//                     flight.  The run of a row is summed by the chunk that it
+//                     begins in, past the border if need be, and written at
+//                     once; only a run longer than a chunk is cut at the
+//                     borders and leaves fp32 partial sums (at most two a
+//                     chunk).  Further CTAs of the same launch write the zeros
+//                     of the rows without a token, so that every output byte
+//                     is written once;
+//   k_rb_join         the runs longer than a chunk: their partial sums in order
+//                     (a padding id may fill thousands of chunks).
 // Short batches (n <= kRbDirectMax) need no sort: k_rb_direct has one CTA per
 // (token, 1,024 columns), and the first token of a row sums the others'.
 #pragma once
@@ -39,15 +38,33 @@ constexpr int kRbThreads = 128;
 constexpr int kRbSliceCols = kRbThreads * 8;
 constexpr int kRbDirectMax = 128;
 constexpr int kRbRankMax = 8192;
-constexpr int kRbRankKeys = 64;  // keys a rank CTA places
+constexpr int kRbRankKeys = 32;  // keys a rank CTA places
 constexpr int kRbRankThreads = 256;
 constexpr int kRbZeroRows = 32;
 constexpr int kRbMaxChunk = 128;
-constexpr int kRbTile = 2048;  // keys of a radix CTA
+constexpr int kRbCluster = 8;
+constexpr int kRbSortThreads = 1024;
 constexpr int kRbDigitBits = 9;
 constexpr int kRbBins = 1 << kRbDigitBits;
-constexpr int kRbJoinThreads = 512;
-constexpr int kRbJoinCols = 256;
+constexpr size_t kRbSortSmem = (1 + kRbSortThreads / 32) * kRbBins * 4;
+constexpr int kRbJoinThreads = 256;
+
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// barrier of all threads of the cluster; earlier writes are visible after it
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *p of CTA r of the cluster (p: the place in this CTA's shared memory)
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, unsigned r) {
+    uint32_t at, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(r));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
 
 struct RbIds {
     const void* ids;
@@ -65,6 +82,25 @@ __device__ __forceinline__ int rb_key(const RbIds& p, long long i) {
     return (id >= p.first_row && d < static_cast<unsigned long long>(p.rows)) ? static_cast<int>(d) : p.rows;
 }
 
+// Rows of tokens i, i + step, ..; past the end: `pad`.  All loads go out before the first is used.
+template <int N>
+__device__ __forceinline__ void rb_keys(const RbIds& p, long long i, int step, long long end, int pad, int (&key)[N]) {
+    long long id[N];
+    if (p.id64) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) id[k] = i + k * step < end ? __ldg(static_cast<const long long*>(p.ids) + i + k * step) : 0;
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) id[k] = i + k * step < end ? __ldg(static_cast<const int*>(p.ids) + i + k * step) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const unsigned long long d = static_cast<unsigned long long>(id[k]) - static_cast<unsigned long long>(p.first_row);
+        key[k] = i + k * step >= end ? pad
+                 : (id[k] >= p.first_row && d < static_cast<unsigned long long>(p.rows)) ? static_cast<int>(d) : p.rows;
+    }
+}
+
 // ------------------------------------------------------------------ sorting
 struct RbRankParams {
     RbIds ids;
@@ -73,138 +109,165 @@ struct RbRankParams {
     int32_t* order;  // out: their tokens
 };
 
+// Lane = key, the warps share the comparisons; keys before and behind the
+// CTA's own need one comparison each, since ties go by position.
 __global__ void __launch_bounds__(kRbRankThreads) k_rb_rank(const __grid_constant__ RbRankParams p) {
+    constexpr int W = kRbRankThreads / 32;
     __shared__ __align__(16) int s_key[kRbRankMax];
-    __shared__ int s_part[kRbRankThreads];
-    const int tid = threadIdx.x;
+    __shared__ int s_part[W][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
-    const int npad = (p.n + 15) & ~15;
-    for (int i = tid; i < npad; i += kRbRankThreads) s_key[i] = i < p.n ? rb_key(p.ids, i) : 0x7FFFFFFF;
-    __syncthreads();
-    // thread (k, q): key k of this CTA against the q-th quarter of all keys
-    const int k = tid % kRbRankKeys, q = tid / kRbRankKeys;
-    const int base = blockIdx.x * kRbRankKeys, me = base + k;
-    const int key = me < p.n ? s_key[me] : 0;
-    const int quarter = npad >> 2;  // a multiple of 4
-    int cnt = 0;
-    for (int j = q * quarter; j < (q + 1) * quarter; j += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(s_key + j);
-        if (j + 4 <= base) {  // all before this CTA's keys: ties come first
-            cnt += (v.x <= key) + (v.y <= key) + (v.z <= key) + (v.w <= key);
-        } else if (j >= base + kRbRankKeys) {
-            cnt += (v.x < key) + (v.y < key) + (v.z < key) + (v.w < key);
-        } else {
-            cnt += (v.x < key || (v.x == key && j < me)) + (v.y < key || (v.y == key && j + 1 < me)) +
-                   (v.z < key || (v.z == key && j + 2 < me)) + (v.w < key || (v.w == key && j + 3 < me));
-        }
+    const int npad = (p.n + 4 * W - 1) / (4 * W) * (4 * W);
+    for (int i = tid; i < npad; i += 8 * kRbRankThreads) {
+        int k[8];
+        rb_keys(p.ids, i, kRbRankThreads, p.n, 0x7FFFFFFF, k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j * kRbRankThreads < npad) s_key[i + j * kRbRankThreads] = k[j];
     }
-    s_part[tid] = cnt;
     __syncthreads();
-    if (q == 0 && me < p.n) {
-        const int at = s_part[k] + s_part[k + kRbRankKeys] + s_part[k + 2 * kRbRankKeys] + s_part[k + 3 * kRbRankKeys];
+    const int base = blockIdx.x * 32, me = base + lane;
+    const int key = me < p.n ? s_key[me] : 0;
+    const int each = npad / W, j0 = warp * each, j1 = j0 + each;  // multiples of 4
+    int cnt = 0;
+    const int mid0 = min(max(base, j0), j1), mid1 = min(max(base + 32, j0), j1);
+#pragma unroll 4
+    for (int j = j0; j < mid0; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(s_key + j);
+        cnt += (v.x <= key) + (v.y <= key) + (v.z <= key) + (v.w <= key);
+    }
+    for (int j = mid0; j < mid1; ++j) cnt += s_key[j] < key || (s_key[j] == key && j < me);
+#pragma unroll 4
+    for (int j = mid1; j < j1; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(s_key + j);
+        cnt += (v.x < key) + (v.y < key) + (v.z < key) + (v.w < key);
+    }
+    s_part[warp][lane] = cnt;
+    __syncthreads();
+    if (warp == 0 && me < p.n) {
+        int at = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) at += s_part[w][lane];
         p.keys[at] = key;
         p.order[at] = me;
     }
 }
 
-struct RbRadixParams {
+struct RbSortParams {
     RbIds ids;
     long long n;
-    const int32_t* keys_in;  // NULL: the ids, in token order
-    const int32_t* order_in;
-    int32_t* keys;
-    int32_t* order;
-    uint32_t* hist;  // [CTA][kRbBins]
-    int32_t shift;
-    int32_t mask;
+    int32_t* keys[2];   // pass i writes [i & 1]
+    int32_t* order[2];
+    int32_t passes, digit;
 };
 
-__global__ void __launch_bounds__(256) k_rb_hist(const __grid_constant__ RbRadixParams p) {
-    __shared__ uint32_t s_h[kRbBins];
-    for (int i = threadIdx.x; i < kRbBins; i += 256) s_h[i] = 0;
-    __syncthreads();
-    pdl_wait();
-    pdl_launch_dependents();
-    const long long t0 = static_cast<long long>(blockIdx.x) * kRbTile;
-    for (int i = threadIdx.x; i < kRbTile; i += 256) {
-        if (t0 + i >= p.n) break;
-        const int key = p.keys_in ? p.keys_in[t0 + i] : rb_key(p.ids, t0 + i);
-        atomicAdd(&s_h[(key >> p.shift) & p.mask], 1u);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRbBins; i += 256) p.hist[static_cast<size_t>(blockIdx.x) * kRbBins + i] = s_h[i];
-}
-
-__global__ void __launch_bounds__(256) k_rb_scatter(const __grid_constant__ RbRadixParams p) {
-    __shared__ uint32_t s_w[8][kRbBins];
-    __shared__ uint32_t s_base[kRbBins];
-    __shared__ uint32_t s_scan[8];
+// Stable radix sort by one cluster of 8 CTAs (the largest portable size): every
+// warp owns a contiguous range of keys, counts its digits, and the counts of
+// all warps give each its places.  The CTAs read one another's counts through
+// the cluster's shared memory and meet at the cluster barrier, so a pass needs
+// no launch of its own.
+__global__ void __cluster_dims__(kRbCluster, 1, 1) __launch_bounds__(kRbSortThreads)
+    k_rb_sort(const __grid_constant__ RbSortParams p) {
+    extern __shared__ __align__(16) uint32_t s_sort[];
+    uint32_t* s_total = s_sort;                      // [kRbBins] of this CTA
+    uint32_t* s_warp = s_sort + kRbBins;             // [warps][kRbBins]
+    __shared__ uint32_t s_scan[kRbSortThreads / 32];
+    constexpr int W = kRbSortThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < 8 * kRbBins; i += 256) (&s_w[0][0])[i] = 0;
-    __syncthreads();
-    pdl_wait();
-    pdl_launch_dependents();
-    const long long t0 = static_cast<long long>(blockIdx.x) * kRbTile + 256 * warp;
-    int key[8], dig[8];
-    unsigned peers[8];
+    const unsigned rank = cluster_rank();
+    const int bins = 1 << p.digit;
+    // keys a warp, a multiple of 32; the warps of all CTAs in order
+    const long long per = (p.n + 32ll * W * kRbCluster - 1) / (32ll * W * kRbCluster) * 32;
+    const long long t0 = (static_cast<long long>(rank) * W + warp) * per, t1 = min(p.n, t0 + per);
+    uint32_t* mine = s_warp + warp * kRbBins;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.digit;
+        const int32_t* kin = p.keys[(pass & 1) ^ 1];
+        const int32_t* oin = p.order[(pass & 1) ^ 1];
+        int32_t* kout = p.keys[pass & 1];
+        int32_t* oout = p.order[pass & 1];
+        auto load = [&](long long t, int (&key)[4]) {  // 128 keys, through L2: other SMs wrote them
+            if (pass == 0) {
+                rb_keys(p.ids, t + lane, 32, t1, -1, key);
+                return;
+            }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const long long i = t0 + 32 * j + lane;
-        key[j] = i < p.n ? (p.keys_in ? p.keys_in[i] : rb_key(p.ids, i)) : 0;
-        dig[j] = i < p.n ? ((key[j] >> p.shift) & p.mask) : kRbBins;  // lanes past the end match only each other
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        peers[j] = __match_any_sync(0xFFFFFFFFu, dig[j]);
-        if (dig[j] < kRbBins && (peers[j] & lanemask_lt()) == 0) s_w[warp][dig[j]] += __popc(peers[j]);
+            for (int i = 0; i < 4; ++i) key[i] = t + 32 * i + lane < t1 ? __ldcg(kin + t + 32 * i + lane) : -1;
+        };
+        for (int i = lane; i < bins; i += 32) mine[i] = 0;
         __syncwarp();
-    }
-    // first place of this CTA's keys of every bin: smaller bins of all CTAs, then this bin's earlier CTAs
-    uint32_t total[2] = {0, 0}, before[2] = {0, 0};
-    for (unsigned c = 0; c < gridDim.x; ++c) {
+        for (long long t = t0; t < t1; t += 128) {
+            int key[4];
+            load(t, key);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t v = p.hist[static_cast<size_t>(c) * kRbBins + 2 * tid + h];
-            if (c < blockIdx.x) before[h] += v;
-            total[h] += v;
+            for (int i = 0; i < 4; ++i) {
+                if (t + 32 * i >= t1) break;
+                const int d = key[i] < 0 ? bins : (key[i] >> shift) & (bins - 1);
+                const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
+                if (d < bins && (peers & lanemask_lt()) == 0) mine[d] += __popc(peers);
+                __syncwarp();
+            }
         }
-    }
-    const uint32_t mine = total[0] + total[1];
-    uint32_t run = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, run, d);
-        if (lane >= d) run += v;
-    }
-    if (lane == 31) s_scan[warp] = run;
-    __syncthreads();
-    uint32_t first = run - mine;
-    for (int w = 0; w < warp; ++w) first += s_scan[w];
-    s_base[2 * tid] = first + before[0];
-    s_base[2 * tid + 1] = first + total[0] + before[1];
-    __syncthreads();
-    for (int b = tid; b < kRbBins; b += 256) {
-        uint32_t at = s_base[b];
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            const uint32_t c = s_w[w][b];
-            s_w[w][b] = at;
-            at += c;
+        __syncthreads();
+        for (int b = tid; b < bins; b += kRbSortThreads) {  // counts before each warp in this CTA
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < W; ++w) {
+                const uint32_t c = s_warp[w * kRbBins + b];
+                s_warp[w * kRbBins + b] = run;
+                run += c;
+            }
+            s_total[b] = run;
         }
-    }
-    __syncthreads();
+        cluster_sync();
+        // first place of this CTA's keys of bin tid: smaller bins of all CTAs, then this bin's earlier CTAs
+        uint32_t total = 0, before = 0;
+        if (tid < bins)
+            for (unsigned r = 0; r < kRbCluster; ++r) {
+                const uint32_t c = cluster_load(s_total + tid, r);
+                if (r < rank) before += c;
+                total += c;
+            }
+        uint32_t run = total;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const long long i = t0 + 32 * j + lane;
-        uint32_t at = 0;
-        if (dig[j] < kRbBins) at = s_w[warp][dig[j]] + __popc(peers[j] & lanemask_lt());
-        __syncwarp();
-        if (dig[j] < kRbBins) {
-            if ((peers[j] & lanemask_lt()) == 0) s_w[warp][dig[j]] += __popc(peers[j]);
-            p.keys[at] = key[j];
-            p.order[at] = p.order_in ? p.order_in[i] : static_cast<int32_t>(i);
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, run, d);
+            if (lane >= d) run += v;
         }
-        __syncwarp();
+        if (lane == 31) s_scan[warp] = run;
+        __syncthreads();
+        uint32_t first = run - total + before;
+        for (int w = 0; w < min(warp, kRbBins / 32); ++w) first += s_scan[w];
+        if (tid < bins) {
+#pragma unroll 8
+            for (int w = 0; w < W; ++w) s_warp[w * kRbBins + tid] += first;
+        }
+        __syncthreads();
+        for (long long t = t0; t < t1; t += 128) {
+            int key[4], tok[4];
+            load(t, key);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long at = t + 32 * i + lane;
+                tok[i] = at < t1 ? (pass ? __ldcg(oin + at) : static_cast<int>(at)) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (t + 32 * i >= t1) break;
+                const int d = key[i] < 0 ? bins : (key[i] >> shift) & (bins - 1);
+                const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
+                const uint32_t at = d < bins ? mine[d] : 0;
+                __syncwarp();
+                if (d < bins) {
+                    const uint32_t to = at + __popc(peers & lanemask_lt());
+                    kout[to] = key[i];
+                    oout[to] = tok[i];
+                    if ((peers & lanemask_lt()) == 0) mine[d] = at + __popc(peers);
+                }
+                __syncwarp();
+            }
+        }
+        cluster_sync();  // the pass is written, and every CTA is done with the counts
     }
 }
 
@@ -295,7 +358,7 @@ __device__ __forceinline__ void rb_zero_rows(void* latent, long long r0, int col
 template <bool kGradF32, bool kLatF32>
 __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ RbSumParams p) {
     constexpr int U = kGradF32 ? 4 : 8;  // rows in flight a thread
-    __shared__ int s_key[kRbMaxChunk + 2], s_tok[kRbMaxChunk];
+    __shared__ int s_key[2 * kRbMaxChunk + 1], s_tok[2 * kRbMaxChunk];
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();
@@ -319,38 +382,55 @@ __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ R
     const int col = static_cast<int>(blockIdx.x - c * p.slices) * kRbSliceCols + 8 * tid;
     const long long p0 = c * p.chunk;
     const int len = static_cast<int>(min(static_cast<long long>(p.chunk), p.n - p0));
-    for (int i = tid; i < len + 2; i += kRbThreads) {  // s_key[i + 1] is the key of place p0 + i
-        const long long at = p0 + i - 1;
-        s_key[i] = (at >= 0 && at < p.n) ? p.keys[at] : -1;
+    // places p0 .. p0 + 2 chunk - 1 (past the end: -1)
+    for (int i = tid; i <= 2 * p.chunk; i += kRbThreads) {
+        const bool on = p0 + i < p.n;
+        s_key[i] = on ? p.keys[p0 + i] : -1;
+        if (i < 2 * p.chunk) s_tok[i] = on ? p.order[p0 + i] : 0;
     }
-    for (int i = tid; i < len; i += kRbThreads) s_tok[i] = p.order[p0 + i];
+    const int before = tid < p.chunk && p0 > tid ? p.keys[p0 - 1 - tid] : -1;
     __syncthreads();
+    // the runs of equal keys that cross this chunk's borders
+    const int k0 = s_key[0], k1 = s_key[len - 1];
+    const int lead = __syncthreads_count(before == k0);                                      // of its first key, before it
+    const int head = __syncthreads_count(tid < len && s_key[tid] == k0);                     // inside
+    const int tail = __syncthreads_count(tid < len && s_key[tid] == k1);                     // of its last key, inside
+    const int past = __syncthreads_count(tid < p.chunk && s_key[len + tid] == k1);           // behind it
+    const bool one_run = k0 == k1;
+    const int more = one_run ? past : 0;
+    // a run longer than a chunk is cut at the borders; a shorter one belongs to the chunk that it begins in
+    const bool lead_long = lead + head + more > p.chunk;
+    int i_begin = 0, i_end = len;
+    if (lead > 0 && !lead_long) i_begin = head;
+    const bool tail_mine = !(one_run && lead > 0);  // the last run begins here
+    const bool tail_long = tail_mine ? tail + past > p.chunk : lead_long;
+    if (tail_mine && !tail_long) i_end = len + past;
     if (col >= p.cols) return;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    bool cut = s_key[0] == s_key[1];  // the current row began in an earlier chunk
-    int start = 0;
-    for (int i0 = 0; i0 < len; i0 += U) {
+    bool cut = lead > 0;  // (of a run that is processed here: a long one)
+    int start = i_begin;
+    if (i_begin > 0) cut = false;
+    for (int i0 = i_begin; i0 < i_end; i0 += U) {
         uint4 v[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool on = i0 + u < len && s_key[i0 + u + 1] < p.ids.rows;
+            const bool on = i0 + u < i_end && s_key[i0 + u] < p.ids.rows;
             if (on) rb_load(p.grad, static_cast<size_t>(s_tok[i0 + u]) * p.cols + col, kGradF32, v[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u;
-            if (i >= len) break;
-            const int key = s_key[i + 1];
+            if (i >= i_end) break;
+            const int key = s_key[i];
             if (key >= p.ids.rows) break;  // ids outside the table sort last
             float f[8];
             rb_floats(v[u], kGradF32, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) acc[q] += f[q];
-            const bool last = i + 1 == len;
-            if (last || s_key[i + 2] != key) {
-                const bool goes_on = last && s_key[i + 2] == key;
+            if (i + 1 == i_end || s_key[i + 1] != key) {
+                const bool goes_on = i + 1 == len && i + 1 == i_end && tail_long && past > 0;
                 if (cut || goes_on) {
                     float4* d = reinterpret_cast<float4*>(p.part + (2 * c + (start == 0 ? 0 : 1)) * p.cols + col);
                     d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -367,20 +447,26 @@ __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ R
     }
 }
 
-// Rows cut by chunk borders: CTA (border b = chunk b | chunk b + 1, 256
-// columns) acts where a cut row's first chunk is b.
+// Runs longer than a chunk: CTA (border b = chunk b | chunk b + 1, 1,024
+// columns) acts where such a run begins in chunk b.  The list of its partial
+// sums is split over two groups of threads.
 template <bool kLatF32>
 __global__ void __launch_bounds__(kRbJoinThreads) k_rb_join(const __grid_constant__ RbSumParams p) {
-    __shared__ __align__(16) float s_sum[kRbJoinThreads / 32][kRbJoinCols];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int G = kRbJoinThreads / kRbThreads;
+    __shared__ __align__(16) float s_sum[G - 1][kRbSliceCols];
+    const int tid = threadIdx.x, part = tid / kRbThreads, at = tid % kRbThreads;
     pdl_wait();
-    const int slices = (p.cols + kRbJoinCols - 1) / kRbJoinCols;
-    const long long b = blockIdx.x / slices;
-    const int col = static_cast<int>(blockIdx.x - b * slices) * kRbJoinCols + 8 * lane;
+    const long long b = blockIdx.x / p.slices;
+    const int col = static_cast<int>(blockIdx.x - b * p.slices) * kRbSliceCols + 8 * at;
     const long long border = (b + 1) * p.chunk;
     const int key = p.keys[border];
-    if (key >= p.ids.rows || p.keys[border - 1] != key) return;
-    if (b > 0 && p.keys[border - p.chunk - 1] == key) return;  // began earlier
+    const int here = tid < p.chunk ? p.keys[border - p.chunk + tid] : -1;
+    const int there = tid < p.chunk && border + tid < p.n ? p.keys[border + tid] : -1;
+    const int earlier = b > 0 ? p.keys[border - p.chunk - 1] : -1;
+    if (key >= p.ids.rows || earlier == key) return;
+    const int tail = __syncthreads_count(here == key);
+    const int past = __syncthreads_count(there == key);
+    if (tail == 0 || tail + past <= p.chunk) return;
     const long long chunks = (p.n + p.chunk - 1) / p.chunk;
     long long lo = b + 1, hi = chunks - 1;  // last chunk that begins with this row
     while (lo < hi) {
@@ -389,31 +475,31 @@ __global__ void __launch_bounds__(kRbJoinThreads) k_rb_join(const __grid_constan
         else hi = mid - 1;
     }
     const long long m = lo - b + 1;  // partial sums
-    const int first_slot = p.keys[b * p.chunk] == key ? 0 : 1;
-    constexpr int W = kRbJoinThreads / 32;
-    const long long per = (m + W - 1) / W;
+    const int first_slot = tail == p.chunk ? 0 : 1;
+    const long long per = (m + G - 1) / G;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     if (col < p.cols) {
-        const long long k1 = min(m, (warp + 1) * per);
-#pragma unroll 4
-        for (long long k = warp * per; k < k1; ++k) {
+        const long long k1 = min(m, (part + 1) * per);
+#pragma unroll 8
+        for (long long k = part * per; k < k1; ++k) {
             const float4* s = reinterpret_cast<const float4*>(p.part + (2 * (b + k) + (k == 0 ? first_slot : 0)) * p.cols + col);
             const float4 x = __ldcs(s), y = __ldcs(s + 1);
             acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
             acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
         }
     }
-    float4* d = reinterpret_cast<float4*>(&s_sum[warp][8 * lane]);
-    d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    if (part > 0) {
+        float4* d = reinterpret_cast<float4*>(&s_sum[part - 1][8 * at]);
+        d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    }
     __syncthreads();
-    if (warp != 0 || col >= p.cols) return;
-    const int used = static_cast<int>((m + per - 1) / per);
-    for (int w = 1; w < used; ++w)
+    if (part != 0 || col >= p.cols) return;
+    for (int w = 0; w < G - 1; ++w)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += s_sum[w][8 * lane + i];
+        for (int i = 0; i < 8; ++i) acc[i] += s_sum[w][8 * at + i];
     rb_store<kLatF32>(p.latent, static_cast<size_t>(key) * p.cols + col, acc, p.alpha, p.accumulate);
 }
 
