@@ -33,7 +33,7 @@
 // before MMA 2 combine at most 32 groups, and the sum of |P_i| over a group is
 // below 28 for core points and core + root (|P| <= sqrt 48 + sqrt 8, sum
 // |P_i| <= sqrt 8 |P|); an overflow point takes part when its sum is at most
-// 64 (32 x 64 = 2,048).  Points farther out (rare), and those past the 64
+// 64 (32 x 64 = 2,048).  Points farther out (rare), and those past the 32
 // that the warp's staging holds, are left out of the f16 path and added in
 // fp32.
 #pragma once
@@ -46,11 +46,11 @@
 
 namespace e8q {
 
-constexpr int kDrWarps = 4;
+constexpr int kDrWarps = 8;
 constexpr int kDrThreads = 32 * kDrWarps;
-constexpr int kDrCtas = 4;  // an SM
+constexpr int kDrCtas = 2;  // an SM
 constexpr int kDrNearSum = 64;  // largest sum of |P_i| of an overflow point in the f16 path
-constexpr int kDrSlots = 64;     // overflow points of a window staged in f16
+constexpr int kDrSlots = 32;     // overflow points of a window staged in f16
 // what is added to a group's codeword, by map entry: 0 none, 1..240 roots, then every warp's staged points, then a void
 constexpr int kDrFirstSlot = 241;
 constexpr int kDrVoid = kDrFirstSlot + kDrWarps * kDrSlots;

@@ -448,8 +448,12 @@ class RowsBackward:
         if grad_dtype not in _DTYPES or latent_dtype not in _DTYPES:
             raise E8qError("gradients must be float32 or bfloat16")
         self.rows, self.cols, self.max_ids = int(rows), int(cols), int(max_ids)
+        if self.rows < 0 or self.cols < 8 or self.max_ids < 0:
+            raise E8qError("rows and max_ids must not be negative, cols at least 8")
         self.grad_dtype, self.latent_dtype = grad_dtype, latent_dtype
-        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.device = torch.device(device if device is not None else "cuda")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         ws = lib().e8q_rows_backward_workspace_bytes(self.max_ids, self.cols)
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
         self.grad_latent = None

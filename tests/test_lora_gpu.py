@@ -267,6 +267,37 @@ def test_adapters_on_other_streams_and_in_graphs(e8q):
             assert torch.equal(a, b)
 
 
+def test_adapters_past_32_bit_offsets(e8q):
+    """The most tokens, and more than 2^31 elements in y and in x (4.3 GB each)."""
+    T, wide = 65536, 32776
+    for cols, rows in ((8, wide), (wide, 8)):
+        g = torch.Generator("cuda").manual_seed(7)
+        a, b = ((torch.randn(s, device="cuda", generator=g) * 0.1).bfloat16() for s in ((2, 8, cols), (2, rows, 8)))
+        x = torch.ones((T, cols), device="cuda", dtype=torch.bfloat16)
+        x[-3:] = 2
+        slots = torch.zeros(T, dtype=torch.int32, device="cuda")
+        slots[-2] = 1
+        op = e8q.Lora(a, b, torch.ones(2, device="cuda"), T)
+        y, u = op(x, slots, keep_u=True)
+        gy = torch.zeros((T, rows), device="cuda", dtype=torch.bfloat16)
+        gy[0], gy[-2:] = 1, 2
+        ga, gb, gx = op.backward(gy, x, u, slots)
+        for t in (0, T // 2, T - 3, T - 2, T - 1):
+            i = int(slots[t])
+            sub = dict(a=a[i:i + 1], b=b[i:i + 1], scale=torch.ones(1, device="cuda"), x=x[t:t + 1], grad_y=gy[t:t + 1],
+                       base=torch.zeros((1, rows), device="cuda"), gx0=torch.zeros((1, cols), device="cuda"),
+                       slots=torch.zeros(1, dtype=torch.int32, device="cuda"))
+            wy, ty, wu, tu = forward64(sub, base=False)
+            close(y[t:t + 1], wy, ty, "y")
+            close(u[t:t + 1], wu, tu, "u")
+            (w1, t1), (w2, t2), (wx, tx) = backward64(sub, u[t:t + 1])
+            close(gx[t:t + 1], wx, tx, "grad_x")
+            if i == 1:  # the only token of its adapter
+                close(ga[1:], w1, t1, "grad_a")
+                close(gb[1:], w2, t2, "grad_b")
+        del x, y, gy, gx, op
+
+
 def test_adapters_refuse_bad_tensors(e8q):
     d = make(10, 64, 72, 16, 3)
     for bad in (dict(a=d["a"].float()), dict(b=d["b"][:, :, :8].contiguous()), dict(scale=d["scale"].double()),

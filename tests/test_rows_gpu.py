@@ -340,6 +340,33 @@ def test_rows_operators_on_other_streams_and_in_graphs(e8q):
         assert torch.equal(lat, e8q.e8q_rows_backward(grad, ids, 50))
 
 
+def test_rows_past_32_bit_offsets(e8q):
+    """More than 2^31 elements on the tokens' side (4.4 GB of bf16)."""
+    m, *_ = encode(e8q, 100, 4096)
+    n = 2 ** 31 // 4096 + 1000
+    ids = torch.arange(n, device="cuda") % 100
+    out = e8q.e8q_decode_rows(m, ids)
+    want = e8q.e8q_decode(m, "original")
+    assert torch.equal(out[-1500:], want[ids[-1500:]]) and torch.equal(out[:100], want)
+    out.fill_(1)
+    out[-1] = 3
+    G = e8q.e8q_rows_backward(out, ids, 100, latent_dtype=torch.float32)  # whole numbers: exact
+    want = torch.bincount(ids, minlength=100).float()
+    want[ids[-1]] += 2
+    assert torch.equal(G, want[:, None].expand(100, 4096))
+
+
+def test_rows_backward_device_argument(e8q):
+    """A device without an index is the current one."""
+    op = e8q.RowsBackward(4, 8, 2, device="cuda")
+    ids = torch.tensor([3, 3], device="cuda")
+    got = op(torch.ones((2, 8), device="cuda").bfloat16(), ids)
+    assert (got[3] == 2).all() and (got[:3] == 0).all()
+    for bad in (dict(rows=-1), dict(cols=0), dict(max_ids=-1), dict(grad_dtype=torch.float16)):
+        with pytest.raises(e8q.E8qError):
+            e8q.RowsBackward(**{**dict(rows=4, cols=8, max_ids=2), **bad})
+
+
 def test_rows_refuse_bad_tensors(e8q):
     m, *_ = encode(e8q, 6, 64)
     ids = torch.zeros(4, dtype=torch.int64, device="cuda")
