@@ -91,16 +91,20 @@ e8q_status ensure_device(int* dev_out) {
         if (st == E8Q_OK)
             st = cuda_ok(cudaFuncSetAttribute(k_rb_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               static_cast<int>(kRbSortSmem)));
-        // the row lookup of the widest rows holds more than the default 48 KB with its signs
-        const int dr_smem = static_cast<int>(dr_smem_bytes(true, kMaxCols));
-        if (st == E8Q_OK)
-            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
-        if (st == E8Q_OK)
-            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
-        if (st == E8Q_OK)
-            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
-        if (st == E8Q_OK)
-            st = cuda_ok(cudaFuncSetAttribute(k_decode_rows<true, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, dr_smem));
+        // the row lookup holds more than the default 48 KB with its stages and signs
+        auto allow_lookup = [&](auto kernel) {
+            if (st == E8Q_OK)
+                st = cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  static_cast<int>(dr_smem_bytes(true, kMaxCols))));
+        };
+        allow_lookup(k_decode_rows<true, true, true>);
+        allow_lookup(k_decode_rows<true, true, false>);
+        allow_lookup(k_decode_rows<true, false, true>);
+        allow_lookup(k_decode_rows<true, false, false>);
+        allow_lookup(k_decode_rows<false, true, true>);
+        allow_lookup(k_decode_rows<false, true, false>);
+        allow_lookup(k_decode_rows<false, false, true>);
+        allow_lookup(k_decode_rows<false, false, false>);
         if (st == E8Q_OK)
             st = cuda_ok(cudaFuncSetAttribute(k_gv_main<1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmemBytes));
         if (st == E8Q_OK)

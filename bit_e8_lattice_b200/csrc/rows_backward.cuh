@@ -222,12 +222,16 @@ __global__ void __cluster_dims__(kRbCluster, 1, 1) __launch_bounds__(kRbSortThre
         cluster_sync();
         // first place of this CTA's keys of bin tid: smaller bins of all CTAs, then this bin's earlier CTAs
         uint32_t total = 0, before = 0;
-        if (tid < bins)
+        if (tid < bins) {
+            uint32_t of[kRbCluster];
+#pragma unroll
+            for (unsigned r = 0; r < kRbCluster; ++r) of[r] = cluster_load(s_total + tid, r);
+#pragma unroll
             for (unsigned r = 0; r < kRbCluster; ++r) {
-                const uint32_t c = cluster_load(s_total + tid, r);
-                if (r < rank) before += c;
-                total += c;
+                if (r < rank) before += of[r];
+                total += of[r];
             }
+        }
         uint32_t run = total;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -467,14 +471,11 @@ __global__ void __launch_bounds__(kRbJoinThreads) k_rb_join(const __grid_constan
     const int tail = __syncthreads_count(here == key);
     const int past = __syncthreads_count(there == key);
     if (tail == 0 || tail + past <= p.chunk) return;
-    const long long chunks = (p.n + p.chunk - 1) / p.chunk;
-    long long lo = b + 1, hi = chunks - 1;  // last chunk that begins with this row
-    while (lo < hi) {
-        const long long mid = (lo + hi + 1) >> 1;
-        if (p.keys[mid * p.chunk] == key) lo = mid;
-        else hi = mid - 1;
+    long long m = 1;  // partial sums: chunk b's, and one of every chunk that begins with this row
+    for (int c = kRbJoinThreads; c == kRbJoinThreads; m += c) {
+        const long long at = (b + m + tid) * p.chunk;
+        c = __syncthreads_count(at < p.n && p.keys[at] == key);
     }
-    const long long m = lo - b + 1;  // partial sums
     const int first_slot = tail == p.chunk ? 0 : 1;
     const long long per = (m + G - 1) / G;
     float acc[8];

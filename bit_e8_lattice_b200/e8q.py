@@ -144,6 +144,8 @@ _ID_TYPES = {torch.int32: E8Q_I32, torch.int64: E8Q_I64}
 
 def _require(t: torch.Tensor, name: str, shape, dtypes, device: torch.device):
     """A contiguous CUDA tensor of this shape and of one of these types, on this device."""
+    if t.dtype in dtypes and t.device == device and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
+        return
     _require_cuda(t, name)
     if t.device != device:
         raise E8qError(f"{name} is on {t.device}, expected {device}")
@@ -156,7 +158,7 @@ def _require(t: torch.Tensor, name: str, shape, dtypes, device: torch.device):
 def _call(what: str, device: torch.device, stream, *args):
     """One library call on the device of its tensors: on `stream`, or on that
     device's current stream."""
-    fn = getattr(lib(), what)
+    fn = getattr(_lib or lib(), what)
     # (torch.cuda.current_stream() builds an object, which takes as long as a launch)
     s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch.cuda.current_device():
@@ -217,12 +219,14 @@ class Encoded:
 
     def c(self) -> EncodedC:
         # an empty record buffer has no address: its row pointers go with it
-        esc = self.esc if self.esc is not None and self.esc.numel() else None
-        ovf = self.ovf if self.ovf is not None and self.ovf.numel() else None
-        return EncodedC(_ptr(self.idx), _ptr(self.scale), _ptr(self.signs), _ptr(esc),
-                        _ptr(self.esc_row_ptr) if esc is not None else None, _ptr(ovf),
-                        _ptr(self.ovf_row_ptr) if ovf is not None else None, self.esc_count, self.ovf_count, self.rows,
-                        self.cols, self.group_base, self.rht_block, 0)
+        def ptr(t):
+            return t.data_ptr() if t is not None else None
+
+        esc = self.esc.data_ptr() if self.esc is not None else None
+        ovf = self.ovf.data_ptr() if self.ovf is not None else None
+        return EncodedC(ptr(self.idx), ptr(self.scale), ptr(self.signs), esc, ptr(self.esc_row_ptr) if esc else None, ovf,
+                        ptr(self.ovf_row_ptr) if ovf else None, self.esc_count, self.ovf_count, self.rows, self.cols,
+                        self.group_base, self.rht_block, 0)
 
 
 @dataclass
@@ -431,7 +435,7 @@ def e8q_decode_rows(m: Encoded, ids: torch.Tensor, basis: str = "original", alph
         with _allocating_on(stream):
             out = torch.empty(ids.shape + (m.cols,), dtype=out_dtype, device=device)
     else:
-        _require(out, "out", ids.shape + (m.cols,), _DTYPES, device)
+        _require(out, "out", tuple(ids.shape) + (m.cols,), _DTYPES, device)
     _call("e8q_decode_rows", device, stream, ctypes.byref(m.c()), DEQUANT[basis], ids.data_ptr(), _ID_TYPES[ids.dtype],
           ids.numel(), int(first_row), float(alpha), out.data_ptr(), _DTYPES[out.dtype])
     return out
