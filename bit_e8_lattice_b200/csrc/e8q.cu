@@ -222,7 +222,7 @@ struct RbPlan {
     int64_t slices;      // of kRbSliceCols columns
     int64_t chunk;       // sorted tokens a summing CTA
     int64_t chunks;
-    size_t keys[2], order[2], part;
+    size_t keys[2], order[2], done, part;
     size_t total;  // workspace; enough for fewer ids too
 };
 
@@ -254,6 +254,7 @@ RbPlan rb_plan(int64_t n, int64_t cols) {
         r.keys[i] = take(static_cast<size_t>(n) * 4);
         r.order[i] = take(static_cast<size_t>(n) * 4);
     }
+    r.done = take(static_cast<size_t>(most) * r.slices * 4);
     r.part = take(static_cast<size_t>(most) * 2 * cols * 4);
     r.total = at;
     return r;
@@ -816,6 +817,8 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
         r.n = static_cast<int32_t>(n);
         r.keys = reinterpret_cast<int32_t*>(w + pl.keys[0]);
         r.order = reinterpret_cast<int32_t*>(w + pl.order[0]);
+        r.done = reinterpret_cast<int32_t*>(w + pl.done);
+        r.dones = static_cast<int32_t>(pl.chunks * pl.slices);
         k_rb_rank<<<static_cast<unsigned>((n + kRbRankKeys - 1) / kRbRankKeys), kRbRankThreads, 0, s>>>(r);
         st = cuda_ok(cudaGetLastError());
     } else {
@@ -825,6 +828,8 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
         RbSortParams r;
         r.ids = q.ids;
         r.n = n;
+        r.done = reinterpret_cast<int32_t*>(w + pl.done);
+        r.dones = pl.chunks * pl.slices;
         r.passes = passes;
         r.digit = digit;
         for (int i = 0; i < 2; ++i) {
@@ -839,18 +844,14 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
     q.keys = reinterpret_cast<const int32_t*>(w + pl.keys[at]);
     q.order = reinterpret_cast<const int32_t*>(w + pl.order[at]);
     q.part = reinterpret_cast<float*>(w + pl.part);
+    q.done = reinterpret_cast<int32_t*>(w + pl.done);
     q.sum_ctas = pl.chunks * pl.slices;
     const int64_t grid = q.sum_ctas + zero_ctas;
     if (grid > 0x7FFFFFFF) return E8Q_ERR_UNSUPPORTED;
-    if (gf && lf) st = launch_pdl(k_rb_sum<true, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
-    else if (gf) st = launch_pdl(k_rb_sum<true, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
-    else if (lf) st = launch_pdl(k_rb_sum<false, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
-    else st = launch_pdl(k_rb_sum<false, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
-    if (st != E8Q_OK || pl.chunks == 1) return st;
-    const int64_t jgrid = (pl.chunks - 1) * pl.slices;
-    if (jgrid > 0x7FFFFFFF) return E8Q_ERR_UNSUPPORTED;
-    return lf ? launch_pdl(k_rb_join<true>, static_cast<int>(jgrid), kRbJoinThreads, 0, s, q)
-              : launch_pdl(k_rb_join<false>, static_cast<int>(jgrid), kRbJoinThreads, 0, s, q);
+    if (gf && lf) return launch_pdl(k_rb_sum<true, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
+    if (gf) return launch_pdl(k_rb_sum<true, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
+    if (lf) return launch_pdl(k_rb_sum<false, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
+    return launch_pdl(k_rb_sum<false, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
 }
 
 }  // extern "C"

@@ -40,10 +40,11 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
 
 // Columns a CTA of k_lr_down: as many as let all CTAs run at once (a second
 // wave would wait for the first), at most 4,096 so that a warp's sum has at
-// most 64 MMAs.  In small batches four CTAs fit an SM and each has little to do.
+// most 64 MMAs.  Small batches take three CTAs an SM (two and four measured 6 %
+// and 8 % slower on 64 tokens of 64 adapters).
 int64_t down_columns(const LrGeom& g, int64_t cols) {
     const int64_t least = ceil_div(cols, 4096), most = ceil_div(cols, 256);
-    const int64_t at_once = 148 * (g.tile == kLrSmallTile ? 4 : 2);
+    const int64_t at_once = 148 * (g.tile == kLrSmallTile ? 3 : 2);
     const int64_t splits = std::min(most, std::max(least, at_once / (g.halves * g.zparts)));
     return ceil_div(ceil_div(cols, splits), 256) * 256;
 }

@@ -2,8 +2,9 @@
 // Figure 2 (b)): every latent row gets the sum of the output gradients of
 // the tokens that read it,
 //   G[r] (+)= alpha * sum_{t : id_t - first_row = r} g[t],
-// in fp32, in token order, rounded once.  Nothing is added with an atomic, so
-// the result does not depend on timing.
+// in fp32, in token order, rounded once.  No sum is formed with an atomic (one
+// counter tells which CTA adds the parts of a long run, always in the same
+// order), so the result does not depend on timing.
 //
 // Tokens are first sorted by row, ties by position:
 //   n <= kRbRankMax   k_rb_rank: the place of a token is the number of tokens
@@ -18,11 +19,11 @@
 //                     begins in, past the border if need be, and written at
 //                     once; only a run longer than a chunk is cut at the
 //                     borders and leaves fp32 partial sums (at most two a
-//                     chunk).  Further CTAs of the same launch write the zeros
-//                     of the rows without a token, so that every output byte
-//                     is written once;
-//   k_rb_join         the runs longer than a chunk: their partial sums in order
-//                     (a padding id may fill thousands of chunks).
+//                     chunk), which the last CTA to write one of the run adds
+//                     in order (a padding id may fill thousands of chunks).
+//                     Further CTAs of the same launch write the zeros of the
+//                     rows without a token, so that every output byte is
+//                     written once.
 // Short batches (n <= kRbDirectMax) need no sort: k_rb_direct has one CTA per
 // (token, 1,024 columns), and the first token of a row sums the others'.
 #pragma once
@@ -39,7 +40,7 @@ constexpr int kRbSliceCols = kRbThreads * 8;
 constexpr int kRbDirectMax = 128;
 constexpr int kRbRankMax = 8192;
 constexpr int kRbRankKeys = 32;  // keys a rank CTA places
-constexpr int kRbRankThreads = 256;
+constexpr int kRbRankThreads = 512;
 constexpr int kRbZeroRows = 32;
 constexpr int kRbMaxChunk = 128;
 constexpr int kRbCluster = 8;
@@ -47,7 +48,6 @@ constexpr int kRbSortThreads = 1024;
 constexpr int kRbDigitBits = 9;
 constexpr int kRbBins = 1 << kRbDigitBits;
 constexpr size_t kRbSortSmem = (1 + kRbSortThreads / 32) * kRbBins * 4;
-constexpr int kRbJoinThreads = 256;
 
 __device__ __forceinline__ unsigned cluster_rank() {
     unsigned r;
@@ -107,6 +107,8 @@ struct RbRankParams {
     int32_t n;
     int32_t* keys;   // out: sorted rows
     int32_t* order;  // out: their tokens
+    int32_t* done;   // out: zeros (RbSumParams)
+    int32_t dones;
 };
 
 // Lane = key, the warps share the comparisons; keys before and behind the
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(kRbRankThreads) k_rb_rank(const __grid_constan
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
     const int npad = (p.n + 4 * W - 1) / (4 * W) * (4 * W);
+    for (int i = blockIdx.x * kRbRankThreads + tid; i < p.dones; i += gridDim.x * kRbRankThreads) p.done[i] = 0;
     for (int i = tid; i < npad; i += 8 * kRbRankThreads) {
         int k[8];
         rb_keys(p.ids, i, kRbRankThreads, p.n, 0x7FFFFFFF, k);
@@ -158,6 +161,8 @@ struct RbSortParams {
     long long n;
     int32_t* keys[2];   // pass i writes [i & 1]
     int32_t* order[2];
+    int32_t* done;      // zeros (RbSumParams)
+    long long dones;
     int32_t passes, digit;
 };
 
@@ -180,6 +185,8 @@ __global__ void __cluster_dims__(kRbCluster, 1, 1) __launch_bounds__(kRbSortThre
     const long long per = (p.n + 32ll * W * kRbCluster - 1) / (32ll * W * kRbCluster) * 32;
     const long long t0 = (static_cast<long long>(rank) * W + warp) * per, t1 = min(p.n, t0 + per);
     uint32_t* mine = s_warp + warp * kRbBins;
+    for (long long i = static_cast<long long>(rank) * kRbSortThreads + tid; i < p.dones; i += kRbCluster * kRbSortThreads)
+        p.done[i] = 0;
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.digit;
         const int32_t* kin = p.keys[(pass & 1) ^ 1];
@@ -282,7 +289,8 @@ struct RbSumParams {
     const int32_t* order;
     const void* grad;
     void* latent;
-    float* part;  // [chunk][2][cols]
+    float* part;    // [chunk][2][cols]
+    int32_t* done;  // [chunk][slice]: partial sums written of the long run that begins in the chunk
     long long n;
     float alpha;
     int32_t cols;
@@ -359,6 +367,47 @@ __device__ __forceinline__ void rb_zero_rows(void* latent, long long r0, int col
     }
 }
 
+// Chunk c has written its part of a run longer than a chunk: whoever writes
+// the last part of the run (in these columns) adds all of them, in order, so
+// that the result does not depend on who that is.  (A launch of its own for
+// this took 6 us.)  Reached by the whole CTA.
+template <bool kLatF32>
+__device__ __forceinline__ void rb_join(const RbSumParams& p, long long c, int key, int col) {
+    const int tid = threadIdx.x;
+    // chunks that begin with this row, back from c and on from c + 1
+    long long back = 0, on = 0;
+    for (int q = kRbThreads; q == kRbThreads; back += q) {
+        const long long k = c - back - tid;
+        q = __syncthreads_count(k >= 0 && p.keys[k * p.chunk] == key);
+    }
+    for (int q = kRbThreads; q == kRbThreads; on += q) {
+        const long long at = (c + 1 + on + tid) * p.chunk;
+        q = __syncthreads_count(at < p.n && p.keys[at] == key);
+    }
+    long long first = c - back + 1;  // the first of them
+    const bool inside = first > 0 && p.keys[first * p.chunk - 1] == key;
+    if (inside) --first;  // the run begins inside the chunk before
+    const int m = static_cast<int>(c + on - first + 1);
+    __shared__ int s_last;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(p.done + first * p.slices + blockIdx.x % p.slices, 1) == m - 1;
+    __syncthreads();
+    if (!s_last || col >= p.cols) return;
+    __threadfence();
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < m; ++k) {
+        const float4* s = reinterpret_cast<const float4*>(p.part + (2 * (first + k) + (k == 0 && inside ? 1 : 0)) * p.cols + col);
+        const float4 x = __ldcg(s), y = __ldcg(s + 1);
+        acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+        acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+    }
+    rb_store<kLatF32>(p.latent, static_cast<size_t>(key) * p.cols + col, acc, p.alpha, p.accumulate);
+}
+
 template <bool kGradF32, bool kLatF32>
 __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ RbSumParams p) {
     constexpr int U = kGradF32 ? 4 : 8;  // rows in flight a thread
@@ -409,7 +458,7 @@ __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ R
     const bool tail_mine = !(one_run && lead > 0);  // the last run begins here
     const bool tail_long = tail_mine ? tail + past > p.chunk : lead_long;
     if (tail_mine && !tail_long) i_end = len + past;
-    if (col >= p.cols) return;
+    const bool col_on = col < p.cols;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -420,7 +469,7 @@ __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ R
         uint4 v[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool on = i0 + u < i_end && s_key[i0 + u] < p.ids.rows;
+            const bool on = col_on && i0 + u < i_end && s_key[i0 + u] < p.ids.rows;
             if (on) rb_load(p.grad, static_cast<size_t>(s_tok[i0 + u]) * p.cols + col, kGradF32, v[u]);
         }
 #pragma unroll
@@ -435,7 +484,8 @@ __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ R
             for (int q = 0; q < 8; ++q) acc[q] += f[q];
             if (i + 1 == i_end || s_key[i + 1] != key) {
                 const bool goes_on = i + 1 == len && i + 1 == i_end && tail_long && past > 0;
-                if (cut || goes_on) {
+                if (!col_on) {
+                } else if (cut || goes_on) {
                     float4* d = reinterpret_cast<float4*>(p.part + (2 * c + (start == 0 ? 0 : 1)) * p.cols + col);
                     d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
                     d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -449,59 +499,11 @@ __global__ void __launch_bounds__(kRbThreads) k_rb_sum(const __grid_constant__ R
             }
         }
     }
-}
-
-// Runs longer than a chunk: CTA (border b = chunk b | chunk b + 1, 1,024
-// columns) acts where such a run begins in chunk b.  The list of its partial
-// sums is split over two groups of threads.
-template <bool kLatF32>
-__global__ void __launch_bounds__(kRbJoinThreads) k_rb_join(const __grid_constant__ RbSumParams p) {
-    constexpr int G = kRbJoinThreads / kRbThreads;
-    __shared__ __align__(16) float s_sum[G - 1][kRbSliceCols];
-    const int tid = threadIdx.x, part = tid / kRbThreads, at = tid % kRbThreads;
-    pdl_wait();
-    const long long b = blockIdx.x / p.slices;
-    const int col = static_cast<int>(blockIdx.x - b * p.slices) * kRbSliceCols + 8 * at;
-    const long long border = (b + 1) * p.chunk;
-    const int key = p.keys[border];
-    const int here = tid < p.chunk ? p.keys[border - p.chunk + tid] : -1;
-    const int there = tid < p.chunk && border + tid < p.n ? p.keys[border + tid] : -1;
-    const int earlier = b > 0 ? p.keys[border - p.chunk - 1] : -1;
-    if (key >= p.ids.rows || earlier == key) return;
-    const int tail = __syncthreads_count(here == key);
-    const int past = __syncthreads_count(there == key);
-    if (tail == 0 || tail + past <= p.chunk) return;
-    long long m = 1;  // partial sums: chunk b's, and one of every chunk that begins with this row
-    for (int c = kRbJoinThreads; c == kRbJoinThreads; m += c) {
-        const long long at = (b + m + tid) * p.chunk;
-        c = __syncthreads_count(at < p.n && p.keys[at] == key);
-    }
-    const int first_slot = tail == p.chunk ? 0 : 1;
-    const long long per = (m + G - 1) / G;
-    float acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    if (col < p.cols) {
-        const long long k1 = min(m, (part + 1) * per);
-#pragma unroll 8
-        for (long long k = part * per; k < k1; ++k) {
-            const float4* s = reinterpret_cast<const float4*>(p.part + (2 * (b + k) + (k == 0 ? first_slot : 0)) * p.cols + col);
-            const float4 x = __ldcs(s), y = __ldcs(s + 1);
-            acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-            acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
-        }
-    }
-    if (part > 0) {
-        float4* d = reinterpret_cast<float4*>(&s_sum[part - 1][8 * at]);
-        d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    }
-    __syncthreads();
-    if (part != 0 || col >= p.cols) return;
-    for (int w = 0; w < G - 1; ++w)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += s_sum[w][8 * at + i];
-    rb_store<kLatF32>(p.latent, static_cast<size_t>(key) * p.cols + col, acc, p.alpha, p.accumulate);
+    // long runs that this chunk has a part of: its first and its last
+    const bool lead_cut = lead > 0 && lead_long && k0 < p.ids.rows;
+    const bool tail_cut = tail_mine && tail_long && past > 0 && k1 < p.ids.rows;
+    if (lead_cut) rb_join<kLatF32>(p, c, k0, col);
+    if (tail_cut) rb_join<kLatF32>(p, c, k1, col);
 }
 
 // Short batches: no sort, one launch.
