@@ -706,6 +706,8 @@ e8q_status e8q_decode_rows(const e8q_encoded* m, int32_t basis, const void* ids,
     if (n > kMaxIds || m->group_base + m->rows * (m->cols / 8) > (int64_t{1} << 32)) return E8Q_ERR_UNSUPPORTED;
     if (n == 0) return E8Q_OK;
     if (!ids || !out || !aligned(ids, id_bytes(id_type)) || !aligned(out, 16)) return E8Q_ERR_INVALID_ARG;
+    if (overlap(ids, static_cast<size_t>(n) * id_bytes(id_type), out, static_cast<size_t>(n) * m->cols * dtype_bytes(out_dtype)))
+        return E8Q_ERR_INVALID_ARG;
     if (m->rows > 0) {
         if (!aligned(m->idx, 2) || !aligned(m->scale, 4)) return E8Q_ERR_INVALID_ARG;
         if (basis == E8Q_DEQUANT_ORIGINAL && (!m->signs || !aligned(m->signs, 8))) return E8Q_ERR_INVALID_ARG;
@@ -846,8 +848,7 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
     q.part = reinterpret_cast<float*>(w + pl.part);
     q.done = reinterpret_cast<int32_t*>(w + pl.done);
     q.sum_ctas = pl.chunks * pl.slices;
-    const int64_t grid = q.sum_ctas + zero_ctas;
-    if (grid > 0x7FFFFFFF) return E8Q_ERR_UNSUPPORTED;
+    const int64_t grid = q.sum_ctas + zero_ctas;  // below 2^28 + 2^25
     if (gf && lf) return launch_pdl(k_rb_sum<true, true>, static_cast<int>(grid), kRbThreads, 0, s, q);
     if (gf) return launch_pdl(k_rb_sum<true, false>, static_cast<int>(grid), kRbThreads, 0, s, q);
     if (lf) return launch_pdl(k_rb_sum<false, true>, static_cast<int>(grid), kRbThreads, 0, s, q);

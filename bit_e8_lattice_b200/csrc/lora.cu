@@ -18,7 +18,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct LrGeom {
     int tile, mt;            // tokens a tile; 16-row tiles of the rank in a k_lr_down CTA
     int64_t tiles;           // most tiles
-    int64_t halves;          // about as many parts of 64 tokens (small batches: tiles)
     int64_t zparts;          // rank parts of k_lr_down
     int64_t unit, units, parts;  // tokens a unit, most units, most partial sums (backward)
 };
@@ -28,7 +27,6 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
     g.tile = tokens <= kLrSmallTokens ? kLrSmallTile : kLrTile;
     // every group (the tokens without an adapter are one) adds at most one tile that is not full
     g.tiles = std::min(tokens, ceil_div(tokens, g.tile) + std::min<int64_t>(tokens, int64_t{a.n} + 1));
-    g.halves = g.tile == kLrSmallTile ? g.tiles : std::min(tokens, ceil_div(tokens, kLrHalf) + std::min<int64_t>(tokens, int64_t{a.n} + 1));
     g.mt = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
     g.zparts = ceil_div(a.rank, 64);
     const int64_t along = ceil_div(a.rows, kLrGradCols) + ceil_div(a.cols, kLrGradCols);
@@ -45,7 +43,7 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
 int64_t down_columns(const LrGeom& g, int64_t cols) {
     const int64_t least = ceil_div(cols, 4096), most = ceil_div(cols, 256);
     const int64_t at_once = 148 * (g.tile == kLrSmallTile ? 3 : 2);
-    const int64_t splits = std::min(most, std::max(least, at_once / (g.halves * g.zparts)));
+    const int64_t splits = std::min(most, std::max(least, at_once / (g.tiles * g.zparts)));
     return ceil_div(ceil_div(cols, splits), 256) * 256;
 }
 
@@ -103,7 +101,7 @@ e8q_status allow_down() {
 
 template <int KS, bool kTrans>
 e8q_status allow_up() {
-    e8q_status st = allow(k_lr_up<KS, kLrHalf, kTrans>, lr_up_smem(KS, kLrHalf, kTrans));
+    e8q_status st = allow(k_lr_up<KS, kLrTile, kTrans>, lr_up_smem(KS, kLrTile, kTrans));
     return st == E8Q_OK ? allow(k_lr_up<KS, kLrSmallTile, kTrans>, lr_up_smem(KS, kLrSmallTile, kTrans)) : st;
 }
 
@@ -172,8 +170,7 @@ e8q_status launch_down(const e8q_adapters& a, const int32_t* slots, const void* 
     p.cols = static_cast<int32_t>(cols);
     p.rank = a.rank;
     p.per = static_cast<int32_t>(down_columns(g, cols));
-    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.per)),
-                    static_cast<unsigned>(g.zparts * (g.tile == kLrSmallTile ? 1 : 2)));
+    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(cols, p.per)), static_cast<unsigned>(g.zparts));
     if (g.tile == kLrSmallTile) {
         const size_t smem = lr_down_few_smem(g.mt, kTrans);
         if (g.mt == 1) return launch_pdl(k_lr_down_few<1, kTrans>, grid, kLrFewThreads, smem, s, p, overlaps);
@@ -191,9 +188,9 @@ e8q_status launch_up_rank(const LrGeom& g, cudaStream_t s, LrUpParams& p) {
     const bool small = g.tile == kLrSmallTile;
     // two rounds of the four CTAs that an SM holds: enough steps to share the factors' preparation, and a short
     // tail (one round: 5 % slower on a 4,096-token prefill)
-    const int64_t parts = std::min(std::max<int64_t>(1, 8 * 148 / g.halves), ceil_div(p.cols, kLrUpCols));
-    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(parts), small ? 1 : 2);
-    constexpr int T = kLrHalf, S = kLrSmallTile;
+    const int64_t parts = std::min(std::max<int64_t>(1, 8 * 148 / g.tiles), ceil_div(p.cols, kLrUpCols));
+    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(parts));
+    constexpr int T = kLrTile, S = kLrSmallTile;
     return small ? launch_pdl(k_lr_up<KS, S, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, S, kTrans), s, p)
                  : launch_pdl(k_lr_up<KS, T, kTrans>, grid, kLrUpThreads, lr_up_smem(KS, T, kTrans), s, p);
 }

@@ -53,7 +53,7 @@ constexpr int kLrMaxAdapters = 2048;
 constexpr int kLrMaxRank = 128;
 constexpr int64_t kLrMaxWidth = 1 << 20;
 constexpr int kLrPlanThreads = 1024;
-constexpr int kLrTile = 128;       // tokens a tile
+constexpr int kLrTile = 64;        // tokens a tile
 constexpr int kLrSmallTile = 8;    // in batches of up to kLrSmallTokens
 constexpr int kLrSmallTokens = 128;
 constexpr int kLrFewThreads = 256;
@@ -464,39 +464,31 @@ __host__ __device__ constexpr size_t lr_down_few_smem(int mt, bool trans) {
     return red > stage ? red : stage;
 }
 
-// Half a tile, up to 64 tokens: z [64][128 columns] and the weights of the same
+// Tiles of up to 64 tokens: z [64][128 columns] and the weights of the same
 // columns come through shared memory, three or four rounds deep (two CTAs an
 // SM: a round's compute is short, and the loads of the next ones have to be
 // out).  8 warps: 4 along the round's columns, 2 along the tokens.
 constexpr int kLrRound = 128;
-constexpr int kLrHalf = 64;
 __host__ __device__ constexpr int lr_down_stages(int mt) { return mt == 4 ? 3 : 4; }
-
-// The half of a tile that a CTA works on; len <= 0: none.
-__device__ __forceinline__ LrTile lr_half(LrTile t, int half) {
-    t.first += kLrHalf * half;
-    t.len = min(t.len - kLrHalf * half, kLrHalf);
-    return t;
-}
 
 template <int MT, bool kTrans>
 __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constant__ LrDownParams p) {
     constexpr int NT = 4, kStages = lr_down_stages(MT);
-    constexpr int ZB = kLrHalf * kLrRound * 2;                           // 16-byte pieces xored with the row
+    constexpr int ZB = kLrTile * kLrRound * 2;                           // 16-byte pieces xored with the row
     constexpr int ROW = MT * 16 * 2 + 16;                                // staged row (kTrans), padded
     constexpr int WB = kTrans ? kLrRound * ROW : MT * 16 * kLrRound * 2;  // (else) pieces xored with the row
     constexpr int STAGE = ZB + WB;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int s_tok[kLrHalf];
+    __shared__ int s_tok[kLrTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
     const int kq = warp & 3, th = warp >> 2;
     pdl_wait();
     pdl_launch_dependents();
     if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
-    const LrTile tile = lr_half(p.tiles[blockIdx.x], blockIdx.z & 1);
-    if (tile.slot < 0 || tile.len <= 0) return;
+    const LrTile tile = p.tiles[blockIdx.x];
+    if (tile.slot < 0) return;
     const int k0 = static_cast<int>(blockIdx.y) * p.per, k1 = min(p.cols, k0 + p.per);
-    const int r0 = static_cast<int>(blockIdx.z >> 1) * 64;
+    const int r0 = static_cast<int>(blockIdx.z) * 64;
     const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
     if (tid < tile.len) s_tok[tid] = p.order[tile.first + tid];
     __syncthreads();
@@ -631,7 +623,7 @@ __global__ void __launch_bounds__(kLrDownThreads) k_lr_down(const __grid_constan
 
 __host__ __device__ constexpr size_t lr_down_smem(int mt, bool trans) {
     const size_t red = size_t{3} * 2 * mt * 16 * 32 * 4;
-    const size_t stages = lr_down_stages(mt) * (size_t{kLrHalf} * kLrRound * 2 + (trans ? kLrRound * (static_cast<size_t>(mt) * 32 + 16)
+    const size_t stages = lr_down_stages(mt) * (size_t{kLrTile} * kLrRound * 2 + (trans ? kLrRound * (static_cast<size_t>(mt) * 32 + 16)
                                                                               : static_cast<size_t>(mt) * 16 * kLrRound * 2));
     return red > stages ? red : stages;
 }
@@ -654,7 +646,7 @@ struct LrUpParams {
 
 // base [tokens][64 columns] and the weights of the same columns come through
 // shared memory, three steps deep; the factors w stay in registers.  TOK: 8
-// tokens (small batches; four warps along the columns), or half a tile of 64
+// tokens (small batches; four warps along the columns), or 64
 // (four warps along the tokens).  Small CTAs, four an SM, because a step is a
 // chain of short waits (copies, barrier, ldmatrix, MMA, store) that only other
 // CTAs fill: 256 threads on 128 columns measured 4 % slower, tiles of 128
@@ -673,7 +665,7 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
     constexpr int STAGE = BB + WB;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ LrSmall s_small;
-    __shared__ int s_rows[kLrHalf];
+    __shared__ int s_rows[kLrTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
     pdl_wait();
     pdl_launch_dependents();
@@ -683,8 +675,7 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
         if (tile.len == 0) return;
     } else {
         if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
-        tile = lr_half(p.tiles[blockIdx.x], blockIdx.z);
-        if (tile.len <= 0) return;
+        tile = p.tiles[blockIdx.x];
         if (tid < tile.len) s_rows[tid] = p.order[tile.first + tid];
         __syncthreads();
     }

@@ -155,12 +155,16 @@ def _require(t: torch.Tensor, name: str, shape, dtypes, device: torch.device):
         raise E8qError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+# (torch.cuda.current_stream() builds an object, which takes as long as a launch)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(what: str, device: torch.device, stream, *args):
     """One library call on the device of its tensors: on `stream`, or on that
     device's current stream."""
     fn = getattr(_lib or lib(), what)
-    # (torch.cuda.current_stream() builds an object, which takes as long as a launch)
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    s = stream.cuda_stream if stream is not None else _current_stream(device.index)
     if device.index == torch.cuda.current_device():
         rc = fn(*args, s)
     else:

@@ -360,7 +360,7 @@ e8q_status e8q_ste_backward(const void* grad_dequant, void* grad_latent, int64_t
  *
  * ids: [n] of id_type (e8q_id_type), aligned to their size; the same id may
  * occur any number of times.  out: [n][cols] bf16 or fp32 (out_dtype),
- * 16-byte aligned.  0 <= n <= 2^30.  alpha finite.  m->signs (original
+ * 16-byte aligned, apart from ids.  0 <= n <= 2^30.  alpha finite.  m->signs (original
  * basis) 8-byte aligned, m->esc 8-byte, m->ovf 4-byte aligned.  Records as
  * for e8q_decode; records outside their row are ignored.
  *

@@ -32,10 +32,10 @@ def matrix(rows=4, cols=64, block=0, **kw):
     (dict(m=dict(signs=P + 4)), 1), (dict(m=dict(idx=None)), 1), (dict(m=dict(idx=P + 1)), 1),
     (dict(m=dict(scale=P + 2)), 1), (dict(m=dict(esc_row_ptr=P)), 1), (dict(m=dict(esc_row_ptr=P, esc=P + 4)), 1),
     (dict(m=dict(ovf_row_ptr=P, ovf=P + 2)), 1), (dict(m=dict(group_base=-1)), 1), (dict(n=0), 0),
-    (dict(n=0, ids=None, out=None), 0),
+    (dict(n=0, ids=None, out=None), 0), (dict(out=P + 16), 1),  # the ids inside out
 ])
 def test_decode_rows_refusals(lib, change, expect):
-    a = dict(m={}, basis=2, ids=P, id_type=1, n=3, first=0, alpha=1.0, out=P, dtype=1)
+    a = dict(m={}, basis=2, ids=P, id_type=1, n=3, first=0, alpha=1.0, out=0x200000, dtype=1)
     a.update(change)
     rc = lib.e8q_decode_rows(ctypes.byref(matrix(**a["m"])), a["basis"], vp(a["ids"]), a["id_type"], a["n"], a["first"],
                              a["alpha"], vp(a["out"]), a["dtype"], None)
