@@ -177,6 +177,36 @@ def test_lookup_without_records_rows_or_ids(e8q):
     assert e8q.e8q_decode_rows(m, ids[:0]).shape == (0, 64)
 
 
+def test_lookup_with_malformed_records(e8q):
+    """Row pointers that are negative, past the records or descending, groups
+    of other rows and roots that do not exist: those records are left out,
+    and rows with sound pointers read as before."""
+    rows, cols = 24, 2048
+    m, *_ = encode(e8q, rows, cols)
+    want = e8q.e8q_decode(m, "original")
+    n_esc, n_ovf = int(m.esc_row_ptr[-1]), int(m.ovf_row_ptr[-1])
+    bare = e8q.Encoded(m.idx, m.scale, m.signs, None, None, None, None, rows, cols, 0, 0)
+    plain = e8q.e8q_decode(bare, "original")  # no record at all
+    ids = torch.arange(rows, device="cuda")
+    for ends in ((-5, -1), (2 ** 62, 2 ** 62 + 9), (n_esc, n_esc + 10 ** 9), (7, 3), (2 ** 32 + 4, 2 ** 32 + 1)):
+        erp, orp = m.esc_row_ptr.clone(), m.ovf_row_ptr.clone()
+        erp[8], erp[9] = ends
+        orp[8], orp[9] = ends
+        bad = e8q.Encoded(m.idx, m.scale, m.signs, m.esc[: 8 * n_esc], erp, m.ovf[: 20 * n_ovf], orp, rows, cols, 0, 0,
+                          n_esc, n_ovf)
+        out = e8q.e8q_decode_rows(bad, ids)
+        assert torch.equal(out[:7], want[:7]) and torch.equal(out[10:], want[10:])
+        assert torch.equal(out[8], plain[8])
+    esc = m.esc[: 8 * n_esc].clone().view(torch.int32).view(-1, 2)
+    ovf = m.ovf[: 20 * n_ovf].clone().view(torch.int32).view(-1, 5)
+    esc[0::2, 0] = -1                 # a group that no row has
+    esc[1::2, 1] |= 0xFF << 16        # root 255
+    ovf[:, 0] += cols // 8            # the next row's group
+    bad = e8q.Encoded(m.idx, m.scale, m.signs, esc.view(torch.uint8).view(-1), m.esc_row_ptr, ovf.view(torch.uint8).view(-1),
+                      m.ovf_row_ptr, rows, cols, 0, 0, n_esc, n_ovf)
+    assert torch.equal(e8q.e8q_decode_rows(bad, ids), plain)
+
+
 def test_lookup_writes_its_rows_only(e8q):
     m, *_ = encode(e8q, 10, 96)
     buf = torch.full((12, 96), 7.0, device="cuda", dtype=torch.bfloat16)
