@@ -667,13 +667,18 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
     __shared__ LrSmall s_small;
     __shared__ int s_rows[kLrTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane & 3, c = lane >> 2;
-    pdl_wait();
-    pdl_launch_dependents();
     LrTile tile;
     if (kSmall) {
+        // Grouping and the first stages read the caller's inputs only.  The first kernel of a call starts after
+        // everything before it, so this may go ahead of the wait for the previous kernel.
         tile = lr_find_tile(s_small, p.slots, p.tokens, p.n, blockIdx.x);
-        if (tile.len == 0) return;
+        if (tile.len == 0) {
+            pdl_wait();
+            return;
+        }
     } else {
+        pdl_wait();
+        pdl_launch_dependents();
         if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
         tile = p.tiles[blockIdx.x];
         if (tid < tile.len) s_rows[tid] = p.order[tile.first + tid];
@@ -682,37 +687,7 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
     const int* s_tok = kSmall ? s_small.tok : s_rows;
     // this CTA's steps: every gridDim.y-th, so that the CTAs of a tile work on neighbouring columns of its rows
     const int c0 = static_cast<int>(blockIdx.y) * COLS, c1 = p.cols, next = static_cast<int>(gridDim.y) * COLS;
-    if (tile.slot < 0) {  // tokens without an adapter
-        if (p.sum && blockIdx.y == 0)
-            for (int i = tid; i < tile.len * p.rank; i += kThreads)
-                p.sum[static_cast<size_t>(s_tok[i / p.rank]) * p.rank + i % p.rank] = 0.f;
-        if (p.base == p.out) return;
-        // copied, the loads of two steps out before their stores
-        constexpr int AT_ONCE = kThreads / (COLS / 8), R = (ROWS + AT_ONCE - 1) / AT_ONCE;
-        const int mine = 8 * (tid % (COLS / 8)), first = tid / (COLS / 8);
-        for (int col = c0 + mine; col < c1; col += 2 * next) {
-            uint4 v[2][R];
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const int row = first + AT_ONCE * i, k = col + d * next;
-                    v[d][i] = make_uint4(0, 0, 0, 0);
-                    if (p.base && row < tile.len && k < c1)
-                        v[d][i] = *reinterpret_cast<const uint4*>(p.base + static_cast<size_t>(s_tok[row]) * p.cols + k);
-                }
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const int row = first + AT_ONCE * i, k = col + d * next;
-                    if (row < tile.len && k < c1)
-                        *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(s_tok[row]) * p.cols + k) = v[d][i];
-                }
-        }
-        return;
-    }
-    const uint16_t* w = p.w + static_cast<size_t>(tile.slot) * p.rank * p.cols;
+    const uint16_t* w = p.w + static_cast<size_t>(max(tile.slot, 0)) * p.rank * p.cols;
     const uint32_t sbase = smem_addr(smem);
     const int m0 = kSmall ? 0 : 16 * warp, j0 = kSmall ? 2 * warp : 0;  // the warp's tokens and column tiles
     // this thread's rows of base and out: kSmall one, of 64 threads; else four of its warp's 16
@@ -755,8 +730,43 @@ __global__ void __launch_bounds__(kLrUpThreads) k_lr_up(const __grid_constant__ 
         }
         cp_async_commit();
     };
+    if (tile.slot >= 0)
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) stage(c0 + i * next, i);
+        for (int i = 0; i < kStages - 1; ++i) stage(c0 + i * next, i);
+    if (kSmall) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    if (tile.slot < 0) {  // tokens without an adapter
+        if (p.sum && blockIdx.y == 0)
+            for (int i = tid; i < tile.len * p.rank; i += kThreads)
+                p.sum[static_cast<size_t>(s_tok[i / p.rank]) * p.rank + i % p.rank] = 0.f;
+        if (p.base == p.out) return;
+        // copied, the loads of two steps out before their stores
+        constexpr int AT_ONCE = kThreads / (COLS / 8), R = (ROWS + AT_ONCE - 1) / AT_ONCE;
+        const int mine = 8 * (tid % (COLS / 8)), first = tid / (COLS / 8);
+        for (int col = c0 + mine; col < c1; col += 2 * next) {
+            uint4 v[2][R];
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int row = first + AT_ONCE * i, k = col + d * next;
+                    v[d][i] = make_uint4(0, 0, 0, 0);
+                    if (p.base && row < tile.len && k < c1)
+                        v[d][i] = *reinterpret_cast<const uint4*>(p.base + static_cast<size_t>(s_tok[row]) * p.cols + k);
+                }
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int row = first + AT_ONCE * i, k = col + d * next;
+                    if (row < tile.len && k < c1)
+                        *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(s_tok[row]) * p.cols + k) = v[d][i];
+                }
+        }
+        return;
+    }
 
     // A operands: lane (c, q) holds tokens c and c + 8 of the warp's 16, ranks 16 k + 2q, + 1, + 8, + 9
     unsigned hi[KS][4], lo[KS][4];
