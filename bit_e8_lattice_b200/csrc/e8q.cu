@@ -254,7 +254,7 @@ RbPlan rb_plan(int64_t n, int64_t cols) {
         r.keys[i] = take(static_cast<size_t>(n) * 4);
         r.order[i] = take(static_cast<size_t>(n) * 4);
     }
-    r.done = take(static_cast<size_t>(most) * r.slices * 4);
+    r.done = take(static_cast<size_t>(most) * r.slices * 12);
     r.part = take(static_cast<size_t>(most) * 2 * cols * 4);
     r.total = at;
     return r;
@@ -820,7 +820,7 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
         r.keys = reinterpret_cast<int32_t*>(w + pl.keys[0]);
         r.order = reinterpret_cast<int32_t*>(w + pl.order[0]);
         r.done = reinterpret_cast<int32_t*>(w + pl.done);
-        r.dones = static_cast<int32_t>(pl.chunks * pl.slices);
+        r.dones = static_cast<int32_t>(3 * pl.chunks * pl.slices);
         k_rb_rank<<<static_cast<unsigned>((n + kRbRankKeys - 1) / kRbRankKeys), kRbRankThreads, 0, s>>>(r);
         st = cuda_ok(cudaGetLastError());
     } else {
@@ -831,7 +831,7 @@ e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const voi
         r.ids = q.ids;
         r.n = n;
         r.done = reinterpret_cast<int32_t*>(w + pl.done);
-        r.dones = pl.chunks * pl.slices;
+        r.dones = 3 * pl.chunks * pl.slices;
         r.passes = passes;
         r.digit = digit;
         for (int i = 0; i < 2; ++i) {

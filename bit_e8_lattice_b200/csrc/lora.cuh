@@ -55,6 +55,8 @@ constexpr int64_t kLrMaxWidth = 1 << 20;
 constexpr int kLrPlanThreads = 1024;
 constexpr int kLrTile = 64;        // tokens a tile
 constexpr int kLrSmallTile = 8;    // in batches of up to kLrSmallTokens
+// 128 tokens of 8 adapters, rank 16, 4096 x 4096: 11 us with each CTA grouping
+// for itself, 19 us with k_lr_plan and tiles of 64; one adapter: 11 and 17
 constexpr int kLrSmallTokens = 128;
 constexpr int kLrFewThreads = 256;
 constexpr int kLrDownThreads = 256;

@@ -43,8 +43,11 @@ namespace e8q {
 
 constexpr int kRbThreads = 128;
 constexpr int kRbSliceCols = kRbThreads * 8;
+// 128 ids into 1000 x 2048: 2.4 us without a sort, 7.5 us with (on one row: 9.5 and 9.0)
 constexpr int kRbDirectMax = 128;
+// into 32000 x 1024, 4,096 ids: 12 us ranked, 22 us by the cluster's sort; 8,192: 21 and 24
 constexpr int kRbRankMax = 8192;
+constexpr int kRbGroup = 32;  // parts of a long run that are added together
 constexpr int kRbRankKeys = 32;  // keys a rank CTA places
 constexpr int kRbRankThreads = 512;
 constexpr int kRbZeroRows = 32;
@@ -296,7 +299,8 @@ struct RbSumParams {
     const void* grad;
     void* latent;
     float* part;    // [chunk][2][cols]
-    int32_t* done;  // [chunk][slice]: partial sums written of the long run that begins in the chunk
+    int32_t* done;  // [chunk][slice][3]: of the run that begins in the chunk, its first group's parts written and its
+                    // groups added; of the run that goes on there, the parts written of the group that begins so
     long long n;
     float alpha;
     int32_t cols;
@@ -373,10 +377,12 @@ __device__ __forceinline__ void rb_zero_rows(void* latent, long long r0, int col
     }
 }
 
-// Chunk c has written its part of a run longer than a chunk: whoever writes
-// the last part of the run (in these columns) adds all of them, in order, so
-// that the result does not depend on who that is.  (A launch of its own for
-// this took 6 us.)  Reached by the whole CTA.
+// Chunk c has written its part of a run longer than a chunk.  Whoever writes
+// the last part of a group of kRbGroup (in these columns) adds the group's, in
+// order; whoever adds the last group of the run adds the groups' sums: the
+// result does not depend on who that is, and no sum is longer than a group
+// plus the groups (8,192 ids that are one padding id, 1,024 columns: 32 us, not
+// 120).  A launch of its own for this took 6 us.  Reached by the whole CTA.
 template <bool kLatF32>
 __device__ __forceinline__ void rb_join(const RbSumParams& p, long long c, int key, int col) {
     const int tid = threadIdx.x;
@@ -393,25 +399,46 @@ __device__ __forceinline__ void rb_join(const RbSumParams& p, long long c, int k
     long long first = c - back + 1;  // the first of them
     const bool inside = first > 0 && p.keys[first * p.chunk - 1] == key;
     if (inside) --first;  // the run begins inside the chunk before
-    const int m = static_cast<int>(c + on - first + 1);
+    const int m = static_cast<int>(c + on - first + 1), lead = static_cast<int>(c - first) / kRbGroup * kRbGroup;
+    const int size = min(kRbGroup, m - lead), groups = (m + kRbGroup - 1) / kRbGroup;
     __shared__ int s_last;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(p.done + first * p.slices + blockIdx.x % p.slices, 1) == m - 1;
-    __syncthreads();
-    if (!s_last || col >= p.cols) return;
-    __threadfence();
+    auto last = [&](long long chunk, int level, int all) {  // of `all` arrivals, earlier writes of the others visible
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) s_last = atomicAdd(p.done + 3 * (chunk * p.slices + blockIdx.x % p.slices) + level, 1) == all - 1;
+        __syncthreads();
+        if (s_last) __threadfence();
+        return s_last != 0;
+    };
+    auto place = [&](int k) {  // part k of the run
+        return reinterpret_cast<float4*>(p.part + (2 * (first + k) + (k == 0 && inside ? 1 : 0)) * p.cols + col);
+    };
     float acc[8];
+    auto add = [&](int k0, int step, int count) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        if (col >= p.cols) return;
 #pragma unroll 4
-    for (int k = 0; k < m; ++k) {
-        const float4* s = reinterpret_cast<const float4*>(p.part + (2 * (first + k) + (k == 0 && inside ? 1 : 0)) * p.cols + col);
-        const float4 x = __ldcg(s), y = __ldcg(s + 1);
-        acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-        acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+        for (int k = 0; k < count; ++k) {
+            const float4* s = place(k0 + k * step);
+            const float4 x = __ldcg(s), y = __ldcg(s + 1);
+            acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+            acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+        }
+    };
+    // (a chunk can end one run and begin another: the run's first group has a counter of its own)
+    if (!last(first + lead, lead == 0 ? 0 : 2, size)) return;
+    add(lead, 1, size);
+    if (groups > 1) {
+        if (col < p.cols) {  // in place of the group's first part
+            float4* d = place(lead);
+            d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        }
+        if (!last(first, 1, groups)) return;
+        add(0, kRbGroup, groups);
     }
-    rb_store<kLatF32>(p.latent, static_cast<size_t>(key) * p.cols + col, acc, p.alpha, p.accumulate);
+    if (col < p.cols) rb_store<kLatF32>(p.latent, static_cast<size_t>(key) * p.cols + col, acc, p.alpha, p.accumulate);
 }
 
 template <bool kGradF32, bool kLatF32>

@@ -268,7 +268,7 @@ def test_gradient_matches_float64(e8q, n, rows, cols, gd, ld):
     assert torch.equal(acc[~touched], there[~touched])
 
 
-@pytest.mark.parametrize("n", [100, 128, 129, 1000, 8192, 8200, 40000])
+@pytest.mark.parametrize("n", [100, 128, 129, 1000, 8192, 8200, 40000, 300000])
 def test_gradient_of_one_row_and_of_distinct_rows(e8q, n):
     """All tokens on one row (a padding id), and every row exactly once."""
     cols = 264
