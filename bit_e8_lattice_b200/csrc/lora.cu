@@ -30,9 +30,11 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
     g.mt = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
     g.zparts = ceil_div(a.rank, 64);
     const int64_t along = ceil_div(a.rows, kLrGradCols) + ceil_div(a.cols, kLrGradCols);
-    g.unit = ceil_div(ceil_div(tokens, std::max<int64_t>(1, kAtOnce / along)), 64) * 64;
-    g.units = ceil_div(tokens, g.unit) + std::min<int64_t>(tokens, a.n);
-    g.parts = 2 * ceil_div(tokens, g.unit);  // an adapter of several units has all but one full
+    const int64_t cuts = std::max<int64_t>(1, kAtOnce / along);  // of the tokens into units
+    g.unit = ceil_div(ceil_div(tokens, cuts), 64) * 64;
+    const int64_t full = std::min(cuts, ceil_div(tokens, 64));  // at least ceil(tokens / unit), and growing with the tokens
+    g.units = full + std::min<int64_t>(tokens, a.n);
+    g.parts = 2 * full;  // an adapter of several units has all but one full
     return g;
 }
 
@@ -40,10 +42,10 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
 // wave would wait for the first), at most 4,096 so that a warp's sum has at
 // most 64 MMAs.  Small batches take three CTAs an SM (two and four measured 6 %
 // and 8 % slower on 64 tokens of 64 adapters).
+int64_t down_at_once(const LrGeom& g) { return 148 * (g.tile == kLrSmallTile ? 3 : 2); }
 int64_t down_columns(const LrGeom& g, int64_t cols) {
     const int64_t least = ceil_div(cols, 4096), most = ceil_div(cols, 256);
-    const int64_t at_once = 148 * (g.tile == kLrSmallTile ? 3 : 2);
-    const int64_t splits = std::min(most, std::max(least, at_once / (g.tiles * g.zparts)));
+    const int64_t splits = std::min(most, std::max(least, down_at_once(g) / (g.tiles * g.zparts)));
     return ceil_div(ceil_div(cols, splits), 256) * 256;
 }
 
@@ -51,6 +53,8 @@ struct LrWs {
     size_t head, order, tiles, units, unit_base, part, parts, grads, total;
 };
 
+// Every part is a bound that grows with the tokens, so that a workspace serves
+// smaller calls too.
 LrWs workspace(const e8q_adapters& a, int64_t tokens, const LrGeom& g, bool backward) {
     LrWs w = {};
     size_t at = 0;
@@ -61,12 +65,14 @@ LrWs workspace(const e8q_adapters& a, int64_t tokens, const LrGeom& g, bool back
     };
     w.head = take(16);
     w.order = take(static_cast<size_t>(tokens) * 4);
-    w.tiles = take(static_cast<size_t>(g.tiles) * sizeof(LrTile));
+    const int64_t few = std::min<int64_t>(tokens, kLrSmallTokens);
+    w.tiles = take(static_cast<size_t>(std::max(g.tiles, geometry(a, few).tiles)) * sizeof(LrTile));
     w.units = take(static_cast<size_t>(g.units) * sizeof(LrTile));
     w.unit_base = take(static_cast<size_t>(a.n) * 8);
     const int64_t cols = backward ? a.rows : a.cols;
-    const int64_t splits = ceil_div(cols, down_columns(g, cols));
-    w.part = take(static_cast<size_t>(splits) * tokens * a.rank * 4);
+    // tokens x splits: the splits are the least, or at most down_at_once / tiles with tiles >= tokens / tile
+    const int64_t rows = std::max(tokens * ceil_div(cols, 4096), std::min(tokens * ceil_div(cols, 256), down_at_once(g) * g.tile));
+    w.part = take(static_cast<size_t>(rows) * a.rank * 4);
     if (backward) {
         w.parts = take(static_cast<size_t>(4) * tokens * a.rank * 2);
         w.grads = take(static_cast<size_t>(g.parts) * (a.rows + a.cols) * a.rank * 4);

@@ -581,31 +581,28 @@ class Lora:
         _require(scale, "scale", (self.n,), (torch.float32,), self.device)
         self.a, self.b, self.scale = a, b, scale
         self.max_tokens = int(max_tokens)
-        if self.max_tokens < 0:
-            raise E8qError("max_tokens must not be negative")
+        if not 0 <= self.max_tokens <= 65536:
+            raise E8qError("max_tokens must be 0 to 65536")
         self._workspace = [None, None]
-        self._need = {}  # workspace bytes by (tokens, backward)
         self._buffers = {}
 
     def _c(self) -> AdaptersC:
         return AdaptersC(self.a.data_ptr(), self.b.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.n,
                          self.rank)
 
-    def _ws(self, ad: AdaptersC, tokens: int, backward: int) -> torch.Tensor:
-        need = self._need.get((tokens, backward))
-        if need is None:
-            need = self._need[tokens, backward] = lib().e8q_lora_workspace_bytes(ctypes.byref(ad), tokens, backward)
+    def _ws(self, ad: AdaptersC, backward: int) -> torch.Tensor:
+        """One workspace for calls of any size: a captured call may go on using it."""
         ws = self._workspace[backward]
-        if ws is None or ws.numel() < need:
-            need = max(need, lib().e8q_lora_workspace_bytes(ctypes.byref(ad), self.max_tokens, backward))
+        if ws is None:
+            need = lib().e8q_lora_workspace_bytes(ctypes.byref(ad), self.max_tokens, backward)
             ws = self._workspace[backward] = torch.empty(need, dtype=torch.uint8, device=self.device)
         return ws
 
     def _out(self, name: str, shape, dtype) -> torch.Tensor:
         """The object's buffer for this output, its first rows for a smaller call."""
         t = self._buffers.get(name)
-        if t is None or t.shape[0] < shape[0]:
-            rows = max(self.max_tokens, shape[0]) if name in ("y", "u", "grad_x") else shape[0]
+        if t is None:
+            rows = self.max_tokens if name in ("y", "u", "grad_x") else shape[0]
             t = self._buffers[name] = torch.empty((rows,) + tuple(shape[1:]), dtype=dtype, device=self.device)
         return t if t.shape[0] == shape[0] else t[: shape[0]]
 
@@ -636,7 +633,7 @@ class Lora:
                 u = self._out("u", (tokens, self.rank), torch.float32)
             elif u is not None:
                 _require(u, "u", (tokens, self.rank), (torch.float32,), self.device)
-            ws = self._ws(ad, tokens, 0)
+            ws = self._ws(ad, 0)
         _call("e8q_lora", self.device, stream, ctypes.byref(ad), x.data_ptr(), slots.data_ptr(), tokens,
               base.data_ptr() if base is not None else None, out.data_ptr(), u.data_ptr() if u is not None else None,
               ws.data_ptr(), ws.numel())
@@ -666,7 +663,7 @@ class Lora:
                 elif name != "grad_x" or need_x:
                     t = self._out(name, shape, torch.bfloat16)
                 outs.append(t)
-            ws = self._ws(ad, tokens, 1)
+            ws = self._ws(ad, 1)
         ga, gb, gx = outs
         _call("e8q_lora_backward", self.device, stream, ctypes.byref(ad), grad_y.data_ptr(), x.data_ptr(), u.data_ptr(),
               slots.data_ptr(), tokens, ga.data_ptr(), gb.data_ptr(),

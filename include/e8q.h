@@ -426,7 +426,7 @@ typedef struct e8q_adapters {
 
 /*
  * Workspace bytes e8q_lora (backward = 0) or e8q_lora_backward (otherwise)
- * needs for this many tokens (exact; the same on every device; 256 for
+ * needs for this many tokens or fewer (the same on every device; 256 for
  * arguments the call would reject).  Needs no GPU.
  */
 size_t e8q_lora_workspace_bytes(const e8q_adapters* ad /* host */, int64_t tokens, int32_t backward);

@@ -78,12 +78,16 @@ def test_lora_backward_refusals(lib, change, expect):
 
 
 def test_lora_workspace(lib):
-    """Holds the grouped order and the partial sums; more tokens never need
-    less within one tile size, and the backward pass needs more."""
+    """Holds the grouped order and the partial sums, serves any smaller number
+    of tokens (a captured call goes on using it), and the backward pass needs
+    more."""
     f = lib.e8q_lora_workspace_bytes
-    for kw in (dict(), dict(rank=128, rows=14336, cols=4096), dict(n=0), dict(n=2048, rows=8, cols=8)):
+    sizes = list(range(1, 700)) + list(range(700, 9000, 61)) + [65535, 65536]
+    for kw in (dict(), dict(rank=128, rows=14336, cols=4096), dict(n=0), dict(n=2048, rows=8, cols=8), dict(n=200, cols=14336),
+               dict(n=1, rows=1 << 20, cols=40)):
         a = ctypes.byref(adapters(**kw))
-        for t in (1, 8, 128, 129, 4096, 65536):
-            w, b = f(a, t, 0), f(a, t, 1)
-            assert w % 256 == 0 and b % 256 == 0 and b > w >= 4 * t
+        for backward in (0, 1):
+            got = [f(a, t, backward) for t in sizes]
+            assert got == sorted(got) and all(b % 256 == 0 for b in got) and got[-1] >= 4 * 65536
+        assert all(f(a, t, 1) > f(a, t, 0) >= 4 * t for t in (1, 128, 129, 4096, 65536))
         assert f(a, 65537, 0) == 256 and f(a, -1, 0) == 256 and f(a, 0, 0) == 256

@@ -267,6 +267,32 @@ def test_adapters_on_other_streams_and_in_graphs(e8q):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("cols,rows", [(264, 136), (2304, 264)])
+def test_adapters_replay_after_calls_of_other_sizes(e8q, cols, rows):
+    """One captured call, then eager calls of every size on the same object:
+    the captured one still has its workspace and its outputs."""
+    T = 192
+    d = make(T, cols, rows, 16, 5)
+    op = e8q.Lora(d["a"], d["b"], d["scale"], T)
+    fresh = e8q.Lora(d["a"], d["b"], d["scale"], T)
+    op.backward(d["grad_y"][:1], d["x"][:1], op(d["x"][:1], d["slots"][:1], keep_u=True)[1], d["slots"][:1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, u = op(d["x"][:1], d["slots"][:1], base=d["base"][:1], keep_u=True)
+        grads = op.backward(d["grad_y"][:1], d["x"][:1], u, d["slots"][:1])
+    for t in (T, 130, 129, 128, 127, 100, 64, 40, 9, 2):
+        sizes = (d["x"][:t], fresh(d["x"][:t], d["slots"][:t], keep_u=True)[1], d["slots"][:t])
+        op(sizes[0], sizes[2], base=d["base"][:t], keep_u=True)
+        op.backward(d["grad_y"][:t], *sizes)
+        filler = torch.full((1 << 22,), float("nan"), device="cuda")  # takes any block that was given back
+        graph.replay()
+        torch.cuda.synchronize()
+        wy, wu = fresh(d["x"][:1], d["slots"][:1], base=d["base"][:1], keep_u=True)
+        assert torch.equal(y, wy) and torch.equal(u, wu) and bool(filler.isnan().all())
+        for got, want in zip(grads, fresh.backward(d["grad_y"][:1], d["x"][:1], wu, d["slots"][:1])):
+            assert torch.equal(got, want)
+
+
 def test_adapters_past_32_bit_offsets(e8q):
     """The most tokens, and more than 2^31 elements in y and in x (4.3 GB each)."""
     T, wide = 65536, 32776
@@ -302,7 +328,7 @@ def test_adapters_refuse_bad_tensors(e8q):
     d = make(10, 64, 72, 16, 3)
     for bad in (dict(a=d["a"].float()), dict(b=d["b"][:, :, :8].contiguous()), dict(scale=d["scale"].double()),
                 dict(scale=d["scale"][:2]), dict(a=d["a"].cpu()), dict(a=d["a"][0]), dict(b=d["b"].transpose(1, 2)),
-                dict(max_tokens=-1)):
+                dict(max_tokens=-1), dict(max_tokens=65537)):
         with pytest.raises(e8q.E8qError):
             e8q.Lora(**{**dict(a=d["a"], b=d["b"], scale=d["scale"], max_tokens=10), **bad})
     op = e8q.Lora(d["a"], d["b"], d["scale"], 10)
