@@ -48,29 +48,29 @@ def _lora(name, kind, tokens, cols, rows, rank, adapters, ragged, train=False):
 def listed():
     return [
         # one token of one request: the decode step of a single user
-        _lookup("lookup one token", 1, 32000, 4096, alpha=64.0),
+        _lookup("lookup, one token", 1, 32000, 4096, alpha=64.0),
         # a prefill chunk; weights quantised at kappa = 1 carry records in a fifth of their groups
-        _lookup("lookup prefill", 8192, 32000, 4096, alpha=64.0),
+        _lookup("lookup, prefill", 8192, 32000, 4096, alpha=64.0),
         # a shard of a wider table read in the rotated basis in fp32, odd sizes, half of the ids on other shards
-        _lookup("lookup fp32 shard", 4099, 25011, 768, basis="rotated", out="f32", ids="i32", kappa=0.6, first=12345),
+        _lookup("lookup, shard in fp32", 4099, 25011, 768, basis="rotated", out="f32", ids="i32", kappa=0.6, first=12345),
         # a short fine-tuning batch into a mid-sized table
-        _lgrad("gradient short batch", 96, 1000, 2048),
+        _lgrad("lookup gradient, short batch", 96, 1000, 2048),
         # a training batch of natural-language tokens (a few rows hold most of them)
-        _lgrad("gradient training", 16384, 32000, 4096, alpha=64.0),
+        _lgrad("lookup gradient, training", 16384, 32000, 4096, alpha=64.0),
         # an odd batch with fp32 gradients, into a shard of the table
-        _lgrad("gradient fp32 shard", 5003, 25011, 768, grad="f32", latent="f32", ids="i32", first=12345),
+        _lgrad("lookup gradient, shard in fp32", 5003, 25011, 768, grad="f32", latent="f32", ids="i32", first=12345),
         # one request decoding one token beside a 4096 x 4096 projection
-        _lora("lora one token", "lora", 1, 4096, 4096, 16, 32, False),
+        _lora("adapters, one token", "lora", 1, 4096, 4096, 16, 32, False),
         # a decode batch in which nearly every request has its own adapter, beside the MLP's wide projection
-        _lora("lora decode batch", "lora", 64, 14336, 4096, 16, 64, False),
+        _lora("adapters, decode batch", "lora", 64, 14336, 4096, 16, 64, False),
         # prompts of several requests in one batch; u is kept for the backward pass
-        _lora("lora prefill", "lora", 4096, 4096, 14336, 32, 8, True, train=True),
+        _lora("adapters, prefill", "lora", 4096, 4096, 14336, 32, 8, True, train=True),
         # three small adapters trained at once on an odd batch
-        _lora("lora gradients small", "lora_grad", 257, 2048, 768, 8, 3, True),
+        _lora("adapter gradients, small", "lora_grad", 257, 2048, 768, 8, 3, True),
         # a training step of four adapters
-        _lora("lora gradients four", "lora_grad", 4096, 4096, 14336, 16, 4, True),
+        _lora("adapter gradients, four", "lora_grad", 4096, 4096, 14336, 16, 4, True),
         # one adapter of a high rank on a long batch
-        _lora("lora gradients one", "lora_grad", 8192, 14336, 4096, 64, 1, True),
+        _lora("adapter gradients, one", "lora_grad", 8192, 14336, 4096, 64, 1, True),
     ]
 
 
