@@ -30,7 +30,8 @@ LrGeom geometry(const e8q_adapters& a, int64_t tokens) {
     g.mt = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
     g.zparts = ceil_div(a.rank, 64);
     const int64_t along = ceil_div(a.rows, kLrGradCols) + ceil_div(a.cols, kLrGradCols);
-    const int64_t cuts = std::max<int64_t>(1, kAtOnce / along);  // of the tokens into units
+    // cuts of the tokens into units: as many as run at once, and units of at most kLrUnitMax tokens
+    const int64_t cuts = std::max(std::max<int64_t>(1, kAtOnce / along), ceil_div(tokens, kLrUnitMax));
     g.unit = ceil_div(ceil_div(tokens, cuts), 64) * 64;
     const int64_t full = std::min(cuts, ceil_div(tokens, 64));  // at least ceil(tokens / unit), and growing with the tokens
     g.units = full + std::min<int64_t>(tokens, a.n);
