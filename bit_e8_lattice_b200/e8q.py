@@ -222,15 +222,18 @@ class Encoded:
     ovf_count: int = 0
 
     def c(self) -> EncodedC:
-        # an empty record buffer has no address: its row pointers go with it
+        # An empty record buffer has no address.  Where it claims no record its row pointers go with it; row
+        # pointers without the records they claim go to the library as they are, which refuses them.
         def ptr(t):
             return t.data_ptr() if t is not None else None
 
-        esc = self.esc.data_ptr() if self.esc is not None else None
-        ovf = self.ovf.data_ptr() if self.ovf is not None else None
-        return EncodedC(ptr(self.idx), ptr(self.scale), ptr(self.signs), esc, ptr(self.esc_row_ptr) if esc else None, ovf,
-                        ptr(self.ovf_row_ptr) if ovf else None, self.esc_count, self.ovf_count, self.rows, self.cols,
-                        self.group_base, self.rht_block, 0)
+        def row_ptr(records, count, t):
+            return None if records is not None and records.numel() == 0 and count == 0 else ptr(t)
+
+        return EncodedC(ptr(self.idx), ptr(self.scale), ptr(self.signs), ptr(self.esc),
+                        row_ptr(self.esc, self.esc_count, self.esc_row_ptr), ptr(self.ovf),
+                        row_ptr(self.ovf, self.ovf_count, self.ovf_row_ptr), self.esc_count, self.ovf_count, self.rows,
+                        self.cols, self.group_base, self.rht_block, 0)
 
 
 @dataclass
