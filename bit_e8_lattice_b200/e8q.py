@@ -449,10 +449,11 @@ def e8q_decode_rows(m: Encoded, ids: torch.Tensor, basis: str = "original", alph
 
 
 class RowsBackward:
-    """Pre-allocated workspace for the gradient of e8q_decode_rows: latent
-    rows [rows][cols] from up to max_ids output rows.  The object may be
-    used by one call at a time: calls that may overlap on the GPU (other
-    streams, graphs replayed side by side) need an object each."""
+    """The gradient of e8q_decode_rows: latent rows [rows][cols] from up to
+    max_ids output rows.  The object keeps one workspace for calls of any
+    size, made by the first of them.  It may be used by one call at a time:
+    calls that may overlap on the GPU (other streams, graphs replayed side by
+    side) need an object each."""
 
     def __init__(self, rows: int, cols: int, max_ids: int, grad_dtype=torch.bfloat16, latent_dtype=torch.bfloat16,
                  device=None):
@@ -465,8 +466,7 @@ class RowsBackward:
         self.device = torch.device(device if device is not None else "cuda")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        ws = lib().e8q_rows_backward_workspace_bytes(self.max_ids, self.cols)
-        self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
+        self.workspace = None
         self.grad_latent = None
 
     def __call__(self, grad_out: torch.Tensor, ids: torch.Tensor, grad_latent: Optional[torch.Tensor] = None,
@@ -478,14 +478,18 @@ class RowsBackward:
         _require(grad_out, "grad_out", ids.shape + (self.cols,), (self.grad_dtype,), self.device)
         if n > self.max_ids:
             raise E8qError(f"{n} ids given to an object for {self.max_ids}")
-        if grad_latent is None:
-            if accumulate:
-                raise E8qError("accumulate needs grad_latent")
-            if self.grad_latent is None:
-                self.grad_latent = torch.empty((self.rows, self.cols), dtype=self.latent_dtype, device=self.device)
-            grad_latent = self.grad_latent
-        else:
+        if grad_latent is not None:
             _require(grad_latent, "grad_latent", (self.rows, self.cols), (self.latent_dtype,), self.device)
+        elif accumulate:
+            raise E8qError("accumulate needs grad_latent")
+        with _allocating_on(stream):
+            if self.workspace is None:
+                ws = lib().e8q_rows_backward_workspace_bytes(self.max_ids, self.cols)
+                self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
+            if grad_latent is None:
+                if self.grad_latent is None:
+                    self.grad_latent = torch.empty((self.rows, self.cols), dtype=self.latent_dtype, device=self.device)
+                grad_latent = self.grad_latent
         _call("e8q_rows_backward", self.device, stream, grad_out.data_ptr(), _DTYPES[self.grad_dtype], ids.data_ptr(),
               _ID_TYPES[ids.dtype], n, int(first_row), float(alpha), 1 if accumulate else 0, grad_latent.data_ptr(),
               _DTYPES[self.latent_dtype], self.rows, self.cols, self.workspace.data_ptr(), self.workspace.numel())
