@@ -180,6 +180,32 @@ def _allocating_on(stream):
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
+class _Kept:
+    """Device memory that an object keeps from one call to the next.  It
+    belongs to the stream of the call that first needs it, and is recorded on
+    every further stream that a call uses it on, so that torch's allocator
+    hands it out again only after those calls, too."""
+
+    def __init__(self, device: torch.device):
+        self.device = device
+        self._kept = {}  # name -> (tensor, handles of its streams)
+
+    def get(self, name, shape, dtype, stream) -> torch.Tensor:
+        """The memory of this name, made with this shape where there is none."""
+        handle = stream.cuda_stream if stream is not None else _current_stream(self.device.index)
+        kept = self._kept.get(name)
+        if kept is None:
+            with _allocating_on(stream):
+                t = torch.empty(shape, dtype=dtype, device=self.device)
+            self._kept[name] = (t, {handle})
+            return t
+        t, streams = kept
+        if handle not in streams:
+            t.record_stream(stream if stream is not None else torch.cuda.current_stream(self.device))
+            streams.add(handle)
+        return t
+
+
 def core_table() -> np.ndarray:
     """The library's host-built core table (doubled coordinates), [65536][8]."""
     out = np.zeros((65536, 8), np.int8)
@@ -453,7 +479,8 @@ class RowsBackward:
     max_ids output rows.  The object keeps one workspace for calls of any
     size, made by the first of them.  It may be used by one call at a time:
     calls that may overlap on the GPU (other streams, graphs replayed side by
-    side) need an object each."""
+    side) need an object each.  It may be dropped while a call still runs, but
+    not before a graph that captured one."""
 
     def __init__(self, rows: int, cols: int, max_ids: int, grad_dtype=torch.bfloat16, latent_dtype=torch.bfloat16,
                  device=None):
@@ -466,8 +493,8 @@ class RowsBackward:
         self.device = torch.device(device if device is not None else "cuda")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self.workspace = None
-        self.grad_latent = None
+        self._ws_bytes = None
+        self._kept = _Kept(self.device)
 
     def __call__(self, grad_out: torch.Tensor, ids: torch.Tensor, grad_latent: Optional[torch.Tensor] = None,
                  alpha: float = 1.0, first_row: int = 0, accumulate: bool = False, stream=None) -> torch.Tensor:
@@ -482,17 +509,14 @@ class RowsBackward:
             _require(grad_latent, "grad_latent", (self.rows, self.cols), (self.latent_dtype,), self.device)
         elif accumulate:
             raise E8qError("accumulate needs grad_latent")
-        with _allocating_on(stream):
-            if self.workspace is None:
-                ws = lib().e8q_rows_backward_workspace_bytes(self.max_ids, self.cols)
-                self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
-            if grad_latent is None:
-                if self.grad_latent is None:
-                    self.grad_latent = torch.empty((self.rows, self.cols), dtype=self.latent_dtype, device=self.device)
-                grad_latent = self.grad_latent
+        if self._ws_bytes is None:
+            self._ws_bytes = lib().e8q_rows_backward_workspace_bytes(self.max_ids, self.cols)
+        ws = self._kept.get("workspace", (self._ws_bytes,), torch.uint8, stream)
+        if grad_latent is None:
+            grad_latent = self._kept.get("grad_latent", (self.rows, self.cols), self.latent_dtype, stream)
         _call("e8q_rows_backward", self.device, stream, grad_out.data_ptr(), _DTYPES[self.grad_dtype], ids.data_ptr(),
               _ID_TYPES[ids.dtype], n, int(first_row), float(alpha), 1 if accumulate else 0, grad_latent.data_ptr(),
-              _DTYPES[self.latent_dtype], self.rows, self.cols, self.workspace.data_ptr(), self.workspace.numel())
+              _DTYPES[self.latent_dtype], self.rows, self.cols, ws.data_ptr(), self._ws_bytes)
         return grad_latent
 
 
@@ -574,7 +598,9 @@ class Lora:
     not copied: a training step may change them in place).  The workspace and
     the outputs that a call is not given belong to the object and are
     overwritten by the next call: calls that may overlap on the GPU (other
-    streams, graphs replayed side by side) need an object each."""
+    streams, graphs replayed side by side) need an object each.  It may be
+    dropped while a call still runs, but not before a graph that captured
+    one."""
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, max_tokens: int):
         _require_cuda(a, "a")
@@ -590,28 +616,24 @@ class Lora:
         self.max_tokens = int(max_tokens)
         if not 0 <= self.max_tokens <= 65536:
             raise E8qError("max_tokens must be 0 to 65536")
-        self._workspace = [None, None]
-        self._buffers = {}
+        self._ws_bytes = [None, None]
+        self._kept = _Kept(self.device)
 
     def _c(self) -> AdaptersC:
         return AdaptersC(self.a.data_ptr(), self.b.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.n,
                          self.rank)
 
-    def _ws(self, ad: AdaptersC, backward: int) -> torch.Tensor:
+    def _ws(self, ad: AdaptersC, backward: int, stream) -> torch.Tensor:
         """One workspace for calls of any size: a captured call may go on using it."""
-        ws = self._workspace[backward]
-        if ws is None:
-            need = lib().e8q_lora_workspace_bytes(ctypes.byref(ad), self.max_tokens, backward)
-            ws = self._workspace[backward] = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return ws
+        if self._ws_bytes[backward] is None:
+            self._ws_bytes[backward] = lib().e8q_lora_workspace_bytes(ctypes.byref(ad), self.max_tokens, backward)
+        return self._kept.get(("workspace", backward), (self._ws_bytes[backward],), torch.uint8, stream)
 
-    def _out(self, name: str, shape, dtype) -> torch.Tensor:
+    def _out(self, name: str, shape, dtype, stream) -> torch.Tensor:
         """The object's buffer for this output, its first rows for a smaller call."""
-        t = self._buffers.get(name)
-        if t is None:
-            rows = self.max_tokens if name in ("y", "u", "grad_x") else shape[0]
-            t = self._buffers[name] = torch.empty((rows,) + tuple(shape[1:]), dtype=dtype, device=self.device)
-        return t if t.shape[0] == shape[0] else t[: shape[0]]
+        rows = self.max_tokens if name in ("y", "u", "grad_x") else shape[0]
+        t = self._kept.get(name, (rows, *shape[1:]), dtype, stream)
+        return t if rows == shape[0] else t[: shape[0]]
 
     def _tokens(self, x: torch.Tensor, slots: torch.Tensor) -> int:
         _require(slots, "slots", None, (torch.int32,), self.device)
@@ -631,16 +653,15 @@ class Lora:
         if base is not None:
             _require(base, "base", (tokens, self.rows), (torch.bfloat16,), self.device)
         ad = self._c()
-        with _allocating_on(stream):
-            if out is None:
-                out = self._out("y", (tokens, self.rows), torch.bfloat16)
-            else:
-                _require(out, "out", (tokens, self.rows), (torch.bfloat16,), self.device)
-            if u is None and keep_u:
-                u = self._out("u", (tokens, self.rank), torch.float32)
-            elif u is not None:
-                _require(u, "u", (tokens, self.rank), (torch.float32,), self.device)
-            ws = self._ws(ad, 0)
+        if out is None:
+            out = self._out("y", (tokens, self.rows), torch.bfloat16, stream)
+        else:
+            _require(out, "out", (tokens, self.rows), (torch.bfloat16,), self.device)
+        if u is None and keep_u:
+            u = self._out("u", (tokens, self.rank), torch.float32, stream)
+        elif u is not None:
+            _require(u, "u", (tokens, self.rank), (torch.float32,), self.device)
+        ws = self._ws(ad, 0, stream)
         _call("e8q_lora", self.device, stream, ctypes.byref(ad), x.data_ptr(), slots.data_ptr(), tokens,
               base.data_ptr() if base is not None else None, out.data_ptr(), u.data_ptr() if u is not None else None,
               ws.data_ptr(), ws.numel())
@@ -662,15 +683,14 @@ class Lora:
             _require(grad_x_base, "grad_x_base", (tokens, self.cols), (torch.bfloat16,), self.device)
         outs = []
         ad = self._c()
-        with _allocating_on(stream):
-            for name, t, shape in (("grad_a", grad_a, self.a.shape), ("grad_b", grad_b, self.b.shape),
-                                   ("grad_x", grad_x, (tokens, self.cols))):
-                if t is not None:
-                    _require(t, name, shape, (torch.bfloat16,), self.device)
-                elif name != "grad_x" or need_x:
-                    t = self._out(name, shape, torch.bfloat16)
-                outs.append(t)
-            ws = self._ws(ad, 1)
+        for name, t, shape in (("grad_a", grad_a, self.a.shape), ("grad_b", grad_b, self.b.shape),
+                               ("grad_x", grad_x, (tokens, self.cols))):
+            if t is not None:
+                _require(t, name, shape, (torch.bfloat16,), self.device)
+            elif name != "grad_x" or need_x:
+                t = self._out(name, shape, torch.bfloat16, stream)
+            outs.append(t)
+        ws = self._ws(ad, 1, stream)
         ga, gb, gx = outs
         _call("e8q_lora_backward", self.device, stream, ctypes.byref(ad), grad_y.data_ptr(), x.data_ptr(), u.data_ptr(),
               slots.data_ptr(), tokens, ga.data_ptr(), gb.data_ptr(),

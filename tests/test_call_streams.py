@@ -90,3 +90,59 @@ def test_row_gradient_workspace_belongs_to_the_calls_stream(watched):
     op, grad, ids = rows_backward(e8q)
     op(grad, ids, torch.zeros((10, 64), dtype=torch.bfloat16), stream=SIDE)
     assert [s for s, _ in log.allocated] == [SIDE]
+
+
+def adapters(e8q, tokens=200):
+    a, b = torch.zeros((3, 8, 64), dtype=torch.bfloat16), torch.zeros((3, 40, 8), dtype=torch.bfloat16)
+    op = e8q.Lora(a, b, torch.ones(3), tokens)
+    op.device = torch.device("cuda", 0)
+    return op
+
+
+def run_adapters(op, tokens, stream):
+    x, slots = torch.zeros((tokens, 64), dtype=torch.bfloat16), torch.zeros(tokens, dtype=torch.int32)
+    y, u = op(x, slots, keep_u=True, stream=stream)
+    return [y, u, *op.backward(y, x, u, slots, stream=stream)]
+
+
+def run_rows(op, grad, ids, stream):
+    return [op(grad, ids, stream=stream)]
+
+
+@pytest.mark.parametrize("kind", ["adapters", "row gradient"])
+def test_kept_memory_is_recorded_on_every_stream_that_uses_it(watched, kind):
+    """The first call's stream owns it; a further one is recorded once, also when it is the current stream."""
+    e8q, log = watched
+    if kind == "adapters":
+        op = adapters(e8q)
+
+        def run(stream, tokens=200):
+            return run_adapters(op, tokens, stream)
+    else:
+        op, grad, ids = rows_backward(e8q)
+
+        def run(stream, tokens=200):
+            return run_rows(op, grad[:tokens], ids[:tokens], stream)
+
+    outs = run(SIDE)
+    owned = [t for _, t in log.allocated]
+    assert len(owned) == (7 if kind == "adapters" else 2) and all(s is SIDE for s, _ in log.allocated) and not log.recorded
+    assert all(log.of(t) is SIDE for t in outs)
+
+    def recorded():
+        found = {(s.name, t.data_ptr()) for s, t in log.recorded}
+        assert len(found) == len(log.recorded)
+        log.recorded.clear()
+        return found
+
+    run(SIDE, 100)
+    assert not recorded()
+    run(None, 100)  # a smaller call on the current stream
+    assert recorded() == {("main", t.data_ptr()) for t in owned}
+    run(None)
+    run(SIDE)
+    assert not recorded()
+    with torch.cuda.stream(THIRD):
+        run(None)
+    assert recorded() == {("third", t.data_ptr()) for t in owned}
+    assert len(log.allocated) == len(owned)

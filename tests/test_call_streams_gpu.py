@@ -39,3 +39,47 @@ def test_row_gradient_on_another_stream(e8q, n):
     got = op(grad, ids, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("tokens", [90, 300])
+def test_adapters_dropped_while_a_call_runs_on_another_stream(e8q, tokens):
+    """The object's memory is the first call's stream's; the call that still
+    runs is another stream's.  What is allocated meanwhile is other memory."""
+    from test_lora_gpu import make
+
+    d = make(tokens, 264, 136, 16, 5)
+    op = e8q.Lora(d["a"], d["b"], d["scale"], tokens)
+    y, u = (t.clone() for t in op(d["x"], d["slots"], base=d["base"], keep_u=True))
+    grads = [t.clone() for t in op.backward(d["grad_y"], d["x"], u, d["slots"])]
+    out, uo = torch.empty_like(y), torch.empty_like(u)
+    got = [torch.empty_like(t) for t in grads]
+    size = [t.numel() * t.element_size() for t, _ in op._kept._kept.values()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    op(d["x"], d["slots"], base=d["base"], out=out, u=uo, stream=side)
+    op.backward(d["grad_y"], d["x"], uo, d["slots"], grad_a=got[0], grad_b=got[1], grad_x=got[2], stream=side)
+    del op
+    fillers = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in size]
+    torch.cuda.synchronize()
+    assert torch.equal(out, y) and torch.equal(uo, u) and all(torch.equal(a, b) for a, b in zip(got, grads))
+    assert all(bool((f == 255).all()) for f in fillers)
+
+
+def test_row_gradient_dropped_while_a_call_runs_on_another_stream(e8q):
+    n, rows, cols = 2000, 300, 1024
+    grad, ids = torch.randn((n, cols), device="cuda").bfloat16(), torch.randint(0, rows, (n,), device="cuda")
+    op = e8q.RowsBackward(rows, cols, n)
+    want = op(grad, ids).clone()
+    size = [t.numel() * t.element_size() for t, _ in op._kept._kept.values()]
+    side = torch.cuda.Stream()
+    got = torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    op(grad, ids, got, stream=side)
+    del op
+    fillers = [torch.full((m,), 255, dtype=torch.uint8, device="cuda") for m in size]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(bool((f == 255).all()) for f in fillers)
