@@ -427,7 +427,8 @@ def e8q_project_encode(weights: Sequence[torch.Tensor], signs: Sequence[torch.Te
 
 def e8q_decode(m: Encoded, basis: str = "rotated", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     if out is None:
-        out = torch.empty((m.rows, m.cols), dtype=torch.bfloat16, device=m.idx.device)
+        with _allocating_on(stream):
+            out = torch.empty((m.rows, m.cols), dtype=torch.bfloat16, device=m.idx.device)
     _require_cuda(out, "out")
     mc = m.c()
     _check(lib().e8q_decode(ctypes.byref(mc), DEQUANT[basis], _ptr(out), _stream_handle(stream)), "e8q_decode")
@@ -555,7 +556,8 @@ class Gemv:
 
 
 def e8q_dequant_gemv(m: Encoded, x: torch.Tensor, stream=None) -> torch.Tensor:
-    return Gemv(m, x.shape[0])(x, stream=stream).clone()
+    with _allocating_on(stream):  # the copy of the result, too
+        return Gemv(m, x.shape[0])(x, stream=stream).clone()
 
 
 class Gemm:
@@ -586,7 +588,8 @@ class Gemm:
 
 
 def e8q_dequant_gemm(m: Encoded, x: torch.Tensor, stream=None) -> torch.Tensor:
-    return Gemm(m, x.shape[0])(x, stream=stream).clone()
+    with _allocating_on(stream):  # the copy of the result, too
+        return Gemm(m, x.shape[0])(x, stream=stream).clone()
 
 
 class Lora:

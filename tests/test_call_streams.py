@@ -146,3 +146,54 @@ def test_kept_memory_is_recorded_on_every_stream_that_uses_it(watched, kind):
         run(None)
     assert recorded() == {("third", t.data_ptr()) for t in owned}
     assert len(log.allocated) == len(owned)
+
+
+class Library:
+    """Answers every workspace question with 256 and every call with success, on the stream it is given."""
+
+    def __init__(self, log):
+        self.log = log
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return lambda *a: 256
+
+        def call(*args):
+            s = args[-1].value
+            self.log.calls.append((name, next(x for x in (SIDE, self.log.main) if x.cuda_stream & (2 ** 64 - 1) == s)))
+            return 0
+
+        return call
+
+
+@pytest.fixture
+def library(watched, monkeypatch):
+    e8q, log = watched
+    log.main, log.written = log.current, []
+    clone, copy, zeros = torch.Tensor.clone, torch.Tensor.copy_, torch.zeros
+    note = log.written.append
+    monkeypatch.setattr(e8q, "lib", lambda: Library(log))
+    monkeypatch.setattr(torch.Tensor, "clone", lambda t: (note(log.current), clone(t))[1])
+    monkeypatch.setattr(torch.Tensor, "copy_", lambda t, s: (note(log.current), copy(t, s))[1])
+    monkeypatch.setattr(torch, "zeros", lambda *a, dtype=None, device=None: (note(log.current), zeros(*a, dtype=dtype))[1])
+    return e8q, log
+
+
+def encoded(e8q):
+    some = torch.ones(8, dtype=torch.uint8)
+    return e8q.Encoded(torch.ones((4, 8), dtype=torch.int16), torch.ones(4), torch.ones(64, dtype=torch.int8), some,
+                       torch.ones(5, dtype=torch.int64), some, torch.ones(5, dtype=torch.int64), 4, 64, 0)
+
+
+@pytest.mark.parametrize("stream", [SIDE, None])
+@pytest.mark.parametrize("name", ["e8q_dequant_gemv", "e8q_dequant_gemm", "e8q_decode"])
+def test_one_shot_calls_work_on_their_stream(library, name, stream):
+    """Memory, kernels and the copy of the result on one stream."""
+    e8q, log = library
+    m, on = encoded(e8q), stream or log.main
+    if name == "e8q_decode":
+        e8q.e8q_decode(m, stream=stream)
+    else:
+        getattr(e8q, name)(m, torch.ones((2, 64), dtype=torch.bfloat16), stream=stream)
+    assert log.calls == [(name, on)] and log.allocated and all(s is on for s, _ in log.allocated)
+    assert all(s is on for s in log.written)
