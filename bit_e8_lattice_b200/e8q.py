@@ -176,7 +176,8 @@ def _call(what: str, device: torch.device, stream, *args):
 
 def _allocating_on(stream):
     """Context in which new tensors belong to the stream that a call runs on
-    (torch's allocator hands memory out per stream)."""
+    (torch's allocator hands memory out per stream), and torch's own
+    operations run there."""
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
@@ -360,16 +361,17 @@ class Encoder:
             if tuple(w.shape) != self.shapes[i] or w.dtype != self.in_dtype:
                 raise E8qError(f"weight {i}: expected {self.shapes[i]} {self.in_dtype}, got {tuple(w.shape)} {w.dtype}")
             self._mats[i].w = w.data_ptr()
-        self._load_scales(scales)
+        self._load_scales(scales, stream)
         rc = lib().e8q_project_encode(self._mats, len(self.shapes), ctypes.byref(self._args),
                                       ctypes.c_void_p(self.workspace.data_ptr()), self.workspace.numel(),
                                       _stream_handle(stream))
         _check(rc, "e8q_project_encode")
         return self.result()
 
-    def _load_scales(self, scales):
-        """Given scales go to the scale buffers the kernels read; an encoder
-        built with scale_in must be given them on every call."""
+    def _load_scales(self, scales, stream):
+        """Given scales go to the scale buffers the kernels read, on the
+        call's stream; an encoder built with scale_in must be given them on
+        every call."""
         if not self.scale_in:
             if scales is not None:
                 raise E8qError("scales given to an encoder built without scale_in")
@@ -381,7 +383,8 @@ class Encoder:
         for i, s in enumerate(scales):
             if s.numel() != self.shapes[i][0]:
                 raise E8qError(f"scales {i}: expected {self.shapes[i][0]} values, got {s.numel()}")
-            self.scale[i].copy_(s.reshape(-1))
+            with _allocating_on(stream):
+                self.scale[i].copy_(s.reshape(-1))
 
     def run_noalloc(self, weights: Sequence[torch.Tensor], scales: Optional[Sequence[torch.Tensor]] = None,
                     stream=None) -> EncodeResult:
@@ -396,7 +399,7 @@ class Encoder:
             if tuple(w.shape) != self.shapes[i] or w.dtype != self.in_dtype:
                 raise E8qError(f"weight {i}: expected {self.shapes[i]} {self.in_dtype}, got {tuple(w.shape)} {w.dtype}")
             self._mats[i].w = w.data_ptr()
-        self._load_scales(scales)
+        self._load_scales(scales, stream)
         rc = lib().e8q_project_encode_noalloc(self._mats, len(self.shapes), ctypes.byref(self._args),
                                               _stream_handle(stream))
         _check(rc, "e8q_project_encode_noalloc")
@@ -420,8 +423,9 @@ def e8q_project_encode(weights: Sequence[torch.Tensor], signs: Sequence[torch.Te
     """One-shot project+encode of a batch of matrices (allocates outputs)."""
     if isinstance(weights, torch.Tensor):
         weights, signs = [weights], [signs]
-    enc = Encoder([tuple(w.shape) for w in weights], signs, weights[0].dtype, rht_block, kappa, dequant,
-                  scales is not None, esc_cap, ovf_cap, device=weights[0].device)
+    with _allocating_on(stream):  # the outputs are cleared there, too
+        enc = Encoder([tuple(w.shape) for w in weights], signs, weights[0].dtype, rht_block, kappa, dequant,
+                      scales is not None, esc_cap, ovf_cap, device=weights[0].device)
     return enc(weights, scales, stream)
 
 

@@ -197,3 +197,20 @@ def test_one_shot_calls_work_on_their_stream(library, name, stream):
         getattr(e8q, name)(m, torch.ones((2, 64), dtype=torch.bfloat16), stream=stream)
     assert log.calls == [(name, on)] and log.allocated and all(s is on for s, _ in log.allocated)
     assert all(s is on for s in log.written)
+
+
+@pytest.mark.parametrize("stream", [SIDE, None])
+def test_encode_with_given_scales_works_on_its_stream(library, stream):
+    """The one-shot encode clears its outputs, and any encode copies the given
+    scales, on the stream that the kernel runs on."""
+    e8q, log = library
+    w, signs, on = torch.ones((4, 64)), torch.ones(64, dtype=torch.int8), stream or log.main
+    e8q.e8q_project_encode(w, signs, scales=[torch.ones(4)], esc_cap=64, ovf_cap=64, stream=stream)
+    assert log.calls == [("e8q_project_encode", on)] and all(s is on for s, _ in log.allocated)
+    assert len(log.written) == 3 and all(s is on for s in log.written)
+    enc = e8q.Encoder([(4, 64)], [signs], torch.float32, scale_in=True, esc_cap=64, ovf_cap=64,
+                      device="cpu")
+    for run in (enc, enc.run_noalloc):
+        log.written.clear()
+        run([w], [torch.ones(4)], stream=stream)
+        assert log.written == [on] and log.calls[-1][1] is on
