@@ -93,6 +93,14 @@ e8q_status check(const e8q_adapters* a, int64_t tokens) {
     return E8Q_OK;
 }
 
+// whether a buffer lies in the adapters' own
+bool overlaps_adapters(const e8q_adapters& a, const void* p, size_t bytes) {
+    if (a.n == 0) return false;
+    const size_t each = static_cast<size_t>(a.n) * a.rank * 2;
+    return overlap(p, bytes, a.a, each * a.cols) || overlap(p, bytes, a.b, each * a.rows) ||
+           overlap(p, bytes, a.scale, static_cast<size_t>(a.n) * 4);
+}
+
 size_t plan_smem(int n) { return static_cast<size_t>(n + 2) * 16 + static_cast<size_t>(n + 1) * 64; }
 
 template <typename K>
@@ -251,6 +259,7 @@ e8q_status e8q_lora(const e8q_adapters* a, const void* x, const int32_t* slots, 
         return E8Q_ERR_INVALID_ARG;
     if (u && (overlap(u, ub, x, xb) || overlap(u, ub, y, yb) || overlap(u, ub, slots, sb) || (base && overlap(u, ub, base, yb))))
         return E8Q_ERR_INVALID_ARG;
+    if (overlaps_adapters(*a, y, yb) || (u && overlaps_adapters(*a, u, ub))) return E8Q_ERR_INVALID_ARG;
     const LrGeom g = geometry(*a, tokens);
     const LrWs l = workspace(*a, tokens, g, false);
     if (!ws || ws_bytes < l.total || !aligned(ws, 256)) return E8Q_ERR_WORKSPACE;
@@ -271,18 +280,20 @@ e8q_status e8q_lora_backward(const e8q_adapters* a, const void* grad_y, const vo
     if (st != E8Q_OK) return st;
     const size_t ab = static_cast<size_t>(a->n) * a->rank * a->cols * 2, bb = static_cast<size_t>(a->n) * a->rank * a->rows * 2;
     if (a->n > 0 && (!grad_a || !grad_b || !aligned(grad_a, 16) || !aligned(grad_b, 16))) return E8Q_ERR_INVALID_ARG;
-    if (a->n > 0 && overlap(grad_a, ab, grad_b, bb)) return E8Q_ERR_INVALID_ARG;
+    if (a->n > 0 && (overlap(grad_a, ab, grad_b, bb) || overlaps_adapters(*a, grad_a, ab) || overlaps_adapters(*a, grad_b, bb)))
+        return E8Q_ERR_INVALID_ARG;
     if (tokens > 0) {
         if (!grad_y || !x || !u || !slots || !aligned(grad_y, 16) || !aligned(x, 16) || !aligned(u, 16) ||
             !aligned(slots, 4) || !aligned(grad_x, 16) || !aligned(grad_x_base, 16) || (grad_x_base && !grad_x))
             return E8Q_ERR_INVALID_ARG;
         const size_t xb = static_cast<size_t>(tokens) * a->cols * 2, yb = static_cast<size_t>(tokens) * a->rows * 2;
         const size_t ub = static_cast<size_t>(tokens) * a->rank * 4, sb = static_cast<size_t>(tokens) * 4;
-        const struct { const void* p; size_t n; } ins[] = {{grad_y, yb}, {x, xb}, {u, ub}, {slots, sb}, {a->a, ab}, {a->b, bb}};
+        const struct { const void* p; size_t n; } ins[] = {{grad_y, yb}, {x, xb}, {u, ub}, {slots, sb}};
         for (const auto& i : ins) {
             if (a->n > 0 && (overlap(i.p, i.n, grad_a, ab) || overlap(i.p, i.n, grad_b, bb))) return E8Q_ERR_INVALID_ARG;
             if (grad_x && overlap(i.p, i.n, grad_x, xb)) return E8Q_ERR_INVALID_ARG;
         }
+        if (grad_x && overlaps_adapters(*a, grad_x, xb)) return E8Q_ERR_INVALID_ARG;
         if (grad_x && a->n > 0 && (overlap(grad_x, xb, grad_a, ab) || overlap(grad_x, xb, grad_b, bb))) return E8Q_ERR_INVALID_ARG;
         if (grad_x_base && grad_x_base != grad_x && overlap(grad_x_base, xb, grad_x, xb)) return E8Q_ERR_INVALID_ARG;
         if (grad_x_base && a->n > 0 && (overlap(grad_x_base, xb, grad_a, ab) || overlap(grad_x_base, xb, grad_b, bb)))
