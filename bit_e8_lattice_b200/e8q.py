@@ -496,6 +496,8 @@ class RowsBackward:
             raise E8qError("rows and max_ids must not be negative, cols at least 8")
         self.grad_dtype, self.latent_dtype = grad_dtype, latent_dtype
         self.device = torch.device(device if device is not None else "cuda")
+        if self.device.type != "cuda":
+            raise E8qError(f"the row gradient needs a CUDA device, got {self.device}")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._ws_bytes = None
