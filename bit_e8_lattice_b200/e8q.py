@@ -155,6 +155,14 @@ def _require(t: torch.Tensor, name: str, shape, dtypes, device: torch.device):
         raise E8qError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _int64(v, name: str) -> int:
+    """v as the library takes it (ctypes would drop the bits of larger numbers)."""
+    v = int(v)
+    if not -2 ** 63 <= v < 2 ** 63:
+        raise E8qError(f"{name} must fit 64 bits, got {v}")
+    return v
+
+
 # (torch.cuda.current_stream() builds an object, which takes as long as a launch)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -475,7 +483,7 @@ def e8q_decode_rows(m: Encoded, ids: torch.Tensor, basis: str = "original", alph
     else:
         _require(out, "out", tuple(ids.shape) + (m.cols,), _DTYPES, device)
     _call("e8q_decode_rows", device, stream, ctypes.byref(m.c()), DEQUANT[basis], ids.data_ptr(), _ID_TYPES[ids.dtype],
-          ids.numel(), int(first_row), float(alpha), out.data_ptr(), _DTYPES[out.dtype])
+          ids.numel(), _int64(first_row, "first_row"), float(alpha), out.data_ptr(), _DTYPES[out.dtype])
     return out
 
 
@@ -522,7 +530,7 @@ class RowsBackward:
         if grad_latent is None:
             grad_latent = self._kept.get("grad_latent", (self.rows, self.cols), self.latent_dtype, stream)
         _call("e8q_rows_backward", self.device, stream, grad_out.data_ptr(), _DTYPES[self.grad_dtype], ids.data_ptr(),
-              _ID_TYPES[ids.dtype], n, int(first_row), float(alpha), 1 if accumulate else 0, grad_latent.data_ptr(),
+              _ID_TYPES[ids.dtype], n, _int64(first_row, "first_row"), float(alpha), 1 if accumulate else 0, grad_latent.data_ptr(),
               _DTYPES[self.latent_dtype], self.rows, self.cols, ws.data_ptr(), self._ws_bytes)
         return grad_latent
 
