@@ -401,8 +401,8 @@ size_t e8q_rows_backward_workspace_bytes(int64_t n, int64_t cols);
  * calls that may run at the same time need one each.
  *
  * Arithmetic: fp32 sums, rounded once to latent_dtype.  The order of the sum
- * follows from the ids and the shapes alone (no atomics), so repeated calls
- * give the same bits on any device.  Asynchronous on `stream`; errors:
+ * follows from the ids and the shapes alone (no floating-point atomics), so
+ * repeated calls give the same bits on any device.  Asynchronous on `stream`; errors:
  * INVALID_ARG, UNSUPPORTED (cols > 16384, n or rows > 2^30), WORKSPACE, CUDA.
  */
 e8q_status e8q_rows_backward(const void* grad_out, int32_t grad_dtype, const void* ids, int32_t id_type, int64_t n,
