@@ -263,7 +263,7 @@ class Encoded:
             return t.data_ptr() if t is not None else None
 
         def row_ptr(records, count, t):
-            return None if records is not None and records.numel() == 0 and count == 0 else ptr(t)
+            return None if count == 0 and records is not None and records.numel() == 0 else ptr(t)
 
         return EncodedC(ptr(self.idx), ptr(self.scale), ptr(self.signs), ptr(self.esc),
                         row_ptr(self.esc, self.esc_count, self.esc_row_ptr), ptr(self.ovf),
