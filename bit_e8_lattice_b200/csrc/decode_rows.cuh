@@ -39,11 +39,12 @@
 //
 // Measured: 8,192 rows of 4,096 columns at kappa = 1 (a fifth of the groups
 // have records), original basis, bf16: 36 us for 84 MB, 2.3 TB/s, 35 % of the
-// measured copy bandwidth.  Bound by instructions and latency together (0.52
-// issued a cycle, 16 warps an SM at 124 registers); the codeword gathers take
-// one L1 wavefront per line (the load pipe is 55 % busy).  Copies without the
-// records run in 31 us, with the butterflies after the MMAs in fp32 43 us (64
-// more live values), with the prefetch in registers 55 us (two CTAs fewer).
+// measured copy bandwidth; fp32 52 us, rotated basis 41 (bf16) and 53 (fp32).
+// Bound by instructions and latency together (0.53 issued a cycle, 16 warps an
+// SM at 124 registers); the codeword gathers take one L1 wavefront per line
+// (the load pipe is 55 % busy).  Copies without the records run in 31 us, with
+// the butterflies after the MMAs in fp32 43 us (64 more live values), with the
+// prefetch in registers 55 us (two CTAs fewer).
 #pragma once
 #include <cuda_fp16.h>
 

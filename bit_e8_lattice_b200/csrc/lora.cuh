@@ -24,22 +24,28 @@
 //
 // The fp32 factors u, v enter the tensor cores as a bf16 high part plus a
 // bf16 low part (two MMAs, about 16 bits), so that the only rounding to bf16
-// that counts is the result's (measured error 1.7e-3, the plain rounding's).
+// that counts is the result's (measured error 1.7e-3, the plain rounding's; 0.2 %
+// of the results are the bf16 neighbour of the exact value's rounding, 0.05 %
+// with the factors in fp32).
 //
 // Measured on one B200 (kernel alone, cold L2; bytes of the token matrices):
 //   k_lr_down   4,096 tokens, rank 32, 4096 columns: 13 us (34 MB); rank 16,
 //               14336 columns from B: 24 us (117 MB, 4.9 TB/s); 64 tokens of 64
 //               adapters, 14336 columns: 10 us (29 MB of A)
-//   k_lr_up     4,096 tokens, rank 32, 14336 columns: 64 us (235 MB, 3.7 TB/s);
-//               64 tokens of 64 adapters, 4096 columns: 9 us
-//   k_lr_grad   4,096 tokens, rank 16, 18,432 columns: 37 us (151 MB, 4.1 TB/s);
-//               8,192 tokens, rank 64: 83 us (302 MB, tensor pipe 50 %)
-//   k_lr_plan   8 us at 4,096 tokens, k_lr_split and k_lr_join 5 us each
-// Long kernels are bound by the waits of their pipelines (issue 0.4 to 0.45 a
-// cycle, tensor pipe 14 to 22 %), the high-rank sums over tokens by the tensor
-// pipe; small batches by the latency of two dependent kernels.  Ranks up to
-// 128 leave little for a 128-row tensor-memory tile to do, which is why these
-// are warp-level MMAs fed from registers.
+//   k_lr_up     4,096 tokens, rank 32, 14336 columns: 68 us (235 MB, 3.5 TB/s);
+//               rank 128: 166 us; 8,192 tokens, rank 64, 14336 columns from A:
+//               123 us (470 MB, 3.8 TB/s); 64 tokens of 64 adapters, 4096
+//               columns: 8 us
+//   k_lr_grad   4,096 tokens, rank 16, 18,432 columns: 41 us (151 MB, 3.7 TB/s);
+//               rank 128: 167 us; 8,192 tokens, rank 64: 118 us (302 MB, tensor
+//               pipe 58 %)
+//   k_lr_plan   9 us at 4,096 tokens, k_lr_split and k_lr_join 5 us each
+// Long kernels of low ranks are bound by the waits of their pipelines (issue
+// 0.4 to 0.45 a cycle, tensor pipe 14 to 22 %).  From rank 64 on the token sums
+// wait for the tensor pipe first (58 %), the up kernel for its own steps and
+// the pipe alike (43 %).  Small batches are bound by the latency of two
+// dependent kernels.  All are warp-level MMAs fed from registers; a tcgen05
+// form has not been tried.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -55,8 +61,10 @@ constexpr int64_t kLrMaxWidth = 1 << 20;
 constexpr int kLrPlanThreads = 1024;
 constexpr int kLrTile = 64;        // tokens a tile
 constexpr int kLrSmallTile = 8;    // in batches of up to kLrSmallTokens
-// 128 tokens of 8 adapters, rank 16, 4096 x 4096: 11 us with each CTA grouping
-// for itself, 19 us with k_lr_plan and tiles of 64; one adapter: 11 and 17
+// Rank 16, 4096 x 4096, each CTA grouping for itself at 128 tokens, and
+// k_lr_plan with tiles of 64 at 129: 11.0 and 17.6 us on one adapter, 11.2 and
+// 18.9 on 8, 11.5 and 20.5 on 64.  The times cross somewhere above 128, which
+// is what the grouping's shared arrays (one thread a token) hold.
 constexpr int kLrSmallTokens = 128;
 // Most tokens a unit of k_lr_grad sums in its MMA accumulators (256 MMAs on
 // each, of high and low parts).  The tensor cores cut off what lies below an

@@ -28,9 +28,10 @@
 // (token, 1,024 columns), and the first token of a row sums the others'.
 //
 // Measured: 16,384 bf16 gradients (natural-language-like ids) into a 32000 x
-// 4096 bf16 table: 92 us, of which the sort about 18 and the sums 72 (396 MB
-// read and written once: 5.5 TB/s, 84 % of the measured copy bandwidth); 5,003
-// fp32 gradients of 768 columns into 25,011 rows: 29.5 us (rank 11, sums 18).
+// 4096 bf16 table: 92 us, of which the sort about 18 and the sums 68 to 72 (396
+// MB read and written once: 5.5 TB/s, 84 % of the measured copy bandwidth), 68 us
+// accumulated (5,408 rows touched); 5,003 fp32 gradients of 768 columns into
+// 25,011 rows: 29.5 us (rank 11, sums 19), 24 us accumulated.
 // The sums are bound by HBM; the sort by its barriers (8 SMs).
 #pragma once
 #include <cuda_bf16.h>
