@@ -551,16 +551,22 @@ class Gemv:
     """Pre-allocated workspace and output for y = W~ x from the 2-bit form."""
 
     def __init__(self, m: Encoded, batch: int):
+        _require_cuda(m.idx, "the encoded matrix")
         self.m, self.batch = m, int(batch)
         self._mc = m.c()
-        ws = lib().e8q_gemv_workspace_bytes(ctypes.byref(self._mc), self.batch)
-        self.workspace = torch.empty(ws, dtype=torch.uint8, device=m.idx.device)
-        self.y = torch.empty((self.batch, m.rows), dtype=torch.bfloat16, device=m.idx.device)
+        self._ws_bytes = lib().e8q_gemv_workspace_bytes(ctypes.byref(self._mc), self.batch)
+        self._kept = _Kept(m.idx.device)
+        self.workspace, self.y = self._memory(None)
+
+    def _memory(self, stream):
+        return (self._kept.get("workspace", (self._ws_bytes,), torch.uint8, stream),
+                self._kept.get("y", (self.batch, self.m.rows), torch.bfloat16, stream))
 
     def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         _require_cuda(x, "x")
         if x.dtype != torch.bfloat16 or tuple(x.shape) != (self.batch, self.m.cols):
             raise E8qError(f"x must be bf16 [{self.batch}][{self.m.cols}]")
+        self._memory(stream)
         y = self.y if out is None else out
         rc = lib().e8q_dequant_gemv(ctypes.byref(self._mc), _ptr(x), self.batch, _ptr(y),
                                     ctypes.c_void_p(self.workspace.data_ptr()), self.workspace.numel(),
@@ -579,16 +585,22 @@ class Gemm:
     (many activation rows; the fused tensor-core dequant-GEMM)."""
 
     def __init__(self, m: Encoded, batch: int):
+        _require_cuda(m.idx, "the encoded matrix")
         self.m, self.batch = m, int(batch)
         self._mc = m.c()
-        ws = lib().e8q_gemm_workspace_bytes(ctypes.byref(self._mc), self.batch)
-        self.workspace = torch.empty(ws, dtype=torch.uint8, device=m.idx.device)
-        self.y = torch.empty((self.batch, m.rows), dtype=torch.bfloat16, device=m.idx.device)
+        self._ws_bytes = lib().e8q_gemm_workspace_bytes(ctypes.byref(self._mc), self.batch)
+        self._kept = _Kept(m.idx.device)
+        self.workspace, self.y = self._memory(None)
+
+    def _memory(self, stream):
+        return (self._kept.get("workspace", (self._ws_bytes,), torch.uint8, stream),
+                self._kept.get("y", (self.batch, self.m.rows), torch.bfloat16, stream))
 
     def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         _require_cuda(x, "x")
         if x.dtype != torch.bfloat16 or tuple(x.shape) != (self.batch, self.m.cols):
             raise E8qError(f"x must be bf16 [{self.batch}][{self.m.cols}]")
+        self._memory(stream)
         y = self.y if out is None else out
         rc = lib().e8q_dequant_gemm(ctypes.byref(self._mc), _ptr(x), self.batch, _ptr(y),
                                     ctypes.c_void_p(self.workspace.data_ptr()), self.workspace.numel(),

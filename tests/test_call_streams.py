@@ -214,3 +214,20 @@ def test_encode_with_given_scales_works_on_its_stream(library, stream):
         log.written.clear()
         run([w], [torch.ones(4)], stream=stream)
         assert log.written == [on] and log.calls[-1][1] is on
+
+
+@pytest.mark.parametrize("name", ["Gemv", "Gemm"])
+def test_kept_memory_of_products_is_recorded(library, name):
+    e8q, log = library
+    op = getattr(e8q, name)(encoded(e8q), 2)
+    x = torch.ones((2, 64), dtype=torch.bfloat16)
+    op(x)
+    assert not log.recorded
+    y = op(x, stream=SIDE)
+    op(x, stream=SIDE)
+    assert len(log.allocated) == 2 and {t.data_ptr() for s, t in log.recorded if s is SIDE} == \
+        {t.data_ptr() for _, t in log.allocated} == {y.data_ptr(), op.workspace.data_ptr()}
+    assert len(log.recorded) == 2
+    log.recorded.clear()
+    op(x, out=torch.ones((2, 4), dtype=torch.bfloat16))
+    assert not log.recorded
